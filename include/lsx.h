@@ -67,7 +67,8 @@ enum lsx_status {
   LSX_ERR_WORKSPACE = -6,   /* workspace missing or too small                */
   LSX_ERR_LAUNCH = -7,      /* a CUDA launch or API call failed              */
   LSX_ERR_TIMEOUT = -8,     /* a device-side bounded wait ran out            */
-  LSX_ERR_DEVICE = -9       /* no usable sm_103 device / context             */
+  LSX_ERR_DEVICE = -9,      /* no usable sm_103 device / context             */
+  LSX_ERR_PAGE = -10        /* device: a page, slot or length outside a cache */
 };
 
 typedef struct lsx_tensor {
@@ -336,6 +337,87 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
                      const lsx_tensor* sk, const lsx_tensor* sv, int64_t chunk_len,
                      float scale, const lsx_tensor* o, const lsx_tensor* lse, void* workspace,
                      size_t workspace_bytes, lsx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged caches: keys and values of many sequences in pages of one pool, the
+ * ragged batches of serving.  (Tree Attention page, related work: DeFT,
+ * KV-guided grouping of decode branches; the pages, as fixed-size blocks of
+ * the sequence axis, are chunks in the sense of the conventions above.)
+ *   k_pages, v_pages [P, Hkv, page, D] bf16 views (B = P pages, N = page
+ *     rows, a power of two from 16 to 256; D in {64, 128}); any strides, so
+ *     [P, page, Hkv, D] storage is the same view with other strides.
+ *   block_table: device int32 [batch][max_pages], rows table_stride entries
+ *     apart; position i of sequence b is row i % page of page
+ *     block_table[b][i / page].  max_pages * page < 2^31.
+ *   kv_lens: device int32 [batch], the keys of each sequence, the new tokens'
+ *     own keys among them.
+ * Lengths, tables and slots are read on the device when the call runs, so a
+ * captured graph follows their contents.  What the host cannot check is
+ * checked there: a page number outside [0, P) leaves its keys out (as if
+ * masked), a length beyond the table counts as max_pages * page keys, a
+ * negative length as 0; each but the last records LSX_ERR_PAGE in the status
+ * word.  Rows of a page past a sequence's length are never used, whatever
+ * they hold.  All calls are inference-only (no gradients).
+ *
+ * attn_page_map -- one step's bookkeeping from the request lengths alone.
+ *   ctx_lens, new_lens: int32 [batch] (1 <= batch <= 4096), the keys a
+ *     sequence has and the tokens it gains; negative counts as 0.
+ *   free_pages: int32 [n_free], pages to hand out, in order.  Sequence b takes
+ *     ceil((ctx + new) / page) - ceil(ctx / page) of them, after those of the
+ *     sequences before it, into the next entries of its row of block_table
+ *     (entries that were there stay; -1 where free_pages has run out).
+ *   out: slot_map int64 [n_tokens], token t of the packed new tokens goes to
+ *     row slot % page of page slot / page; -1 past the last token and where
+ *     there is no page or no table entry for it.  cu_new int32 [batch + 1],
+ *     the first packed token of each sequence and their number; kv_lens int32
+ *     [batch] = ctx + new; taken int32 [1], the pages asked for (more than
+ *     n_free: the pool ran out).  The sums have to fit 31 bits.
+ *   Calling it again with the same inputs gives the same results.
+ *
+ * attn_page_append -- writes the new rows into their slots.
+ *   k, v [1, Hkv, T, D] bf16, or f32 (each value rounded once); slot_map
+ *   int64 [T].  Slots < 0 are skipped; a slot past the pool is skipped and
+ *   recorded as LSX_ERR_PAGE.  The slots >= 0 have to be distinct: of two
+ *   tokens with one slot either may remain, in pieces.
+ *
+ * attn_paged_decode -- one or a few query tokens per sequence.
+ *   q [B, Hq, Nq, D] bf16, (Hq / Hkv) * Nq <= 64; query n of sequence b sees
+ *   its keys j <= kv_len - Nq + n (the Nq tokens are its last ones).
+ *   prefix_table: int32, the pages of prefix_len keys that every query sees
+ *   before its own (NULL when prefix_len is 0): a prefix shared by the batch,
+ *   read once for up to 64 query rows together, not once per sequence.
+ *   o [B, Hq, Nq, D] bf16 or f32, lse [B, Hq, Nq, 1] f32; a query without
+ *   keys gets O = 0, LSE = -inf.  P is kept to 16 bits in the P V product.
+ *
+ * attn_paged_fwd -- prompts: ragged query tokens, causal, over the cache.
+ *   q [1, Hq, T, D] bf16, the tokens of sequence b at [cu_q[b], cu_q[b + 1])
+ *   (device int32 [batch + 1], ascending, batch <= 4096); the i-th of its n
+ *   tokens sees keys j <= kv_len - n + i.  Hq / Hkv <= 128.  o, lse as q; rows
+ *   that belong to no sequence are left as they were.  P is rounded to bf16.
+ *
+ * Both need the workspace their *_workspace_size names (256-byte aligned).
+ * ---------------------------------------------------------------------- */
+int attn_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch,
+                  const int32_t* free_pages, int64_t n_free, int64_t page_size,
+                  int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                  int64_t* slot_map, int64_t n_tokens, int32_t* cu_new, int32_t* kv_lens,
+                  int32_t* taken, lsx_stream_t stream);
+int attn_page_append(const lsx_tensor* k, const lsx_tensor* v, const int64_t* slot_map,
+                     const lsx_tensor* k_pages, const lsx_tensor* v_pages, lsx_stream_t stream);
+size_t attn_paged_decode_workspace_size(const lsx_tensor* q, const lsx_tensor* k_pages,
+                                        int64_t max_pages, int64_t prefix_len);
+int attn_paged_decode(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_tensor* v_pages,
+                      const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                      const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
+                      float scale, const lsx_tensor* o, const lsx_tensor* lse, void* workspace,
+                      size_t workspace_bytes, lsx_stream_t stream);
+size_t attn_paged_fwd_workspace_size(const lsx_tensor* q, const lsx_tensor* k_pages,
+                                     int64_t batch, int64_t max_pages);
+int attn_paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_tensor* v_pages,
+                   const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                   const int32_t* kv_lens, const int32_t* cu_q, int64_t batch, float scale,
+                   const lsx_tensor* o, const lsx_tensor* lse, void* workspace,
+                   size_t workspace_bytes, lsx_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Status, diagnostics and host-side helpers.

@@ -28,13 +28,22 @@ from .attention import (  # noqa: F401
     tree_merge,
     version,
 )
+from .paged import (  # noqa: F401
+    page_append,
+    page_map,
+    paged_decode,
+    paged_decode_workspace_size,
+    paged_fwd,
+    paged_fwd_workspace_size,
+)
 from .autograd import ChunkedAttention, chunked_attention  # noqa: F401
 from . import ring  # noqa: F401
 
 __all__ = [
     "chunk_fwd", "chunk_bwd", "chunked_fwd", "chunked_bwd", "block_sparse_fwd",
     "block_sparse_bwd", "merge", "tree_merge",
-    "decode", "decode_tree", "decode_workspace_size", "schedule_stats", "selftest_bounded_wait",
+    "decode", "decode_tree", "decode_workspace_size", "page_append", "page_map", "paged_decode",
+    "paged_decode_workspace_size", "paged_fwd", "paged_fwd_workspace_size", "schedule_stats", "selftest_bounded_wait",
     "set_deterministic", "set_wait_limit_ns", "status_string", "sync_status", "version", "chunked_attention",
     "ChunkedAttention",
 ]

@@ -22,7 +22,7 @@ LSX_F32 = 1
 STATUS = {
     0: "LSX_OK", -1: "LSX_ERR_NULL", -2: "LSX_ERR_SHAPE", -3: "LSX_ERR_DTYPE",
     -4: "LSX_ERR_ALIGN", -5: "LSX_ERR_UNSUPPORTED", -6: "LSX_ERR_WORKSPACE",
-    -7: "LSX_ERR_LAUNCH", -8: "LSX_ERR_TIMEOUT", -9: "LSX_ERR_DEVICE",
+    -7: "LSX_ERR_LAUNCH", -8: "LSX_ERR_TIMEOUT", -9: "LSX_ERR_DEVICE", -10: "LSX_ERR_PAGE",
 }
 
 
@@ -77,6 +77,15 @@ SIGNATURES = {
                                 _P, _P, _P, _VP, _SZ, _VP]),
     "attn_decode_workspace_size": (_SZ, [_P, _P, _I64]),
     "attn_decode": (_INT, [_P, _P, _P, _I64, ctypes.c_float, _P, _P, _VP, _SZ, _VP]),
+    "attn_page_map": (_INT, [_VP, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _VP,
+                             _VP]),
+    "attn_page_append": (_INT, [_P, _P, _VP, _P, _P, _VP]),
+    "attn_paged_decode_workspace_size": (_SZ, [_P, _P, _I64, _I64]),
+    "attn_paged_decode": (_INT, [_P, _P, _P, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _P, _P,
+                                 _VP, _SZ, _VP]),
+    "attn_paged_fwd_workspace_size": (_SZ, [_P, _P, _I64, _I64]),
+    "attn_paged_fwd": (_INT, [_P, _P, _P, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _P, _P,
+                              _VP, _SZ, _VP]),
     "lsx_sync_status": (_INT, [_VP]),
     "lsx_status_string": (ctypes.c_char_p, [_INT]),
     "lsx_set_wait_limit_ns": (None, [ctypes.c_uint64]),

@@ -25,7 +25,8 @@ int device_ctx(DeviceCtx* ctx);
 enum KernelId {
   kKidFwdTc = 0, kKidDkdv, kKidDq, kKidRowDot, kKidMerge, kKidTreeMerge,
   kKidDecode, kKidSimtFwd, kKidSimtBwd, kKidFill, kKidTranspose, kKidBlockLists,
-  kKidBwdFused, kKidDqConvert, kKidCount
+  kKidBwdFused, kKidDqConvert, kKidPageMap, kKidPageAppend, kKidPagedDecode, kKidPagedMerge,
+  kKidPagedFwd, kKidPagedPlan, kKidCount
 };
 
 // Sequence-contiguous copies (layout.cu): a bf16 [B, H, N, D] view is
