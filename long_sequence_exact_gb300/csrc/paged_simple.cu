@@ -128,20 +128,10 @@ int launch_simple(const lsx_tensor& q, const PagedCache& c, int64_t hkv, const i
 
 }  // namespace
 
-size_t paged_decode_workspace(const lsx_tensor&, const lsx_tensor&, int64_t, int64_t, int) {
-  return 0;
-}
 size_t paged_fwd_workspace(const lsx_tensor&, const lsx_tensor&, int64_t, int64_t, int) {
   return 0;
 }
 
-int launch_paged_decode(const lsx_tensor& q, const PagedCache& c, int64_t hkv,
-                        const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
-                        float scale, const lsx_tensor& o, const lsx_tensor& lse, void*,
-                        const DeviceCtx& ctx, cudaStream_t s) {
-  return launch_simple(q, c, hkv, kv_lens, nullptr, q.B, prefix_table, prefix_len, scale, o, lse,
-                       ctx, s, kKidPagedDecode);
-}
 int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor&,
                      const PagedCache& c, const int32_t* kv_lens, const int32_t* cu_q,
                      int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse, void*,
