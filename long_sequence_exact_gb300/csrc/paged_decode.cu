@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "paged.h"
+#include "paged_merge.cuh"
 #include "ptx.cuh"
 
 namespace lsx {
@@ -497,12 +498,10 @@ struct PagedMergeParams {
   lsx_tensor o, lse;
 };
 
-// One warp per output row, lane = D / 32 elements.  The partials of a unit
-// that was cut, in key order (the prefix's first), 32 at a time with their
-// weights in the lanes; rows whose unit was whole are already written.
+// One warp per output row: the partials of a unit that was cut, in key order
+// (the prefix's first); rows whose unit was whole are already written.
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams p) {
-  constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -511,58 +510,17 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams
                 b = row / (p.rows.Nq * p.rows.Hq);
   const int64_t hk = h / p.rows.G;
   const int64_t gr = (b * p.rows.G + h % p.rows.G) * p.rows.Nq + n;
-  float m = kNegInf, tot = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  RowMerge<D> sum;
   auto take = [&](const RunView& v) {
     int64_t first, last;
     bool begins;
     const int64_t u = gr / v.R, r = gr - u * v.R;
     unit_runs(v, u, hk, first, last, begins);
-    for (int64_t c0 = first; c0 <= last; c0 += 32) {
-      const int count = static_cast<int>(last - c0 + 1 < 32 ? last - c0 + 1 : 32);
-      auto slot_of = [&](int i) {
-        return first == last ? v.whole_slot0 + u * v.hkv + hk
-                             : 2 * (c0 + i) + (c0 + i == first && begins ? 1 : 0);
-      };
-      const float mine = lane < count ? __ldcg(v.part.l + slot_of(lane) * v.R + r) : kNegInf;
-      float mx = mine;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-      const float m_new = fmaxf(m, mx);
-      if (m_new == kNegInf) continue;
-      const float keep = m == kNegInf ? 0.f : ex2((m - m_new) * kLog2e);
-      const float w = mine == kNegInf ? 0.f : ex2((mine - m_new) * kLog2e);
-      float sum = w;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      tot = tot * keep + sum;
-      m = m_new;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= keep;
-      for (int i0 = 0; i0 < count; i0 += 8) {
-        float y[8][E];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < count) {
-            const float* src = v.part.o + (slot_of(i0 + i) * v.R + r) * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-              y[i][0] = f.x; y[i][1] = f.y; y[i][2] = f.z; y[i][3] = f.w;
-            } else {
-              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-              y[i][0] = f.x; y[i][1] = f.y;
-            }
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-          if (i0 + i < count)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, y[i][e], acc[e]);
-        }
-      }
-    }
+    sum.take(v.part.o, v.part.l, last - first + 1, lane, [&](int64_t i) {
+      const int64_t slot = first == last ? v.whole_slot0 + u * v.hkv + hk
+                                         : 2 * (first + i) + (i == 0 && begins ? 1 : 0);
+      return slot * v.R + r;
+    });
   };
   if (p.prefix.grid > 0) {
     take(p.prefix);
@@ -573,20 +531,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams
     if (first == last) return;
   }
   take(p.own);
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  const int64_t at = view_off(p.o, b, h, n) + lane * E;
-  if (p.o.dtype == LSX_F32) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) static_cast<float*>(p.o.data)[at + e] = acc[e] * inv;
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o.data) + at + e) =
-          pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  }
-  if (lane == 0)
-    static_cast<float*>(p.lse.data)[view_off(p.lse, b, h, n)] =
-        tot > 0.f ? m + lg2(tot) * kLn2 : kNegInf;
+  sum.store(p.o, p.lse, b, h, n, lane);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }

@@ -1,0 +1,992 @@
+// paged_fwd.cu -- tcgen05 attention of many query tokens against a cache kept
+// in pages: ragged prompts, causal (attn_paged_fwd), and the queries of a
+// decode batch against the prefix they share (attn_paged_decode).  The online
+// softmax of the dense forward (BurstAttention, method section: local attention
+// computation), with pages in the place of chunks.
+//
+// Bound: the tensor cores (4 D operations per visible (query, key) pair), for
+// few tokens the cache's bytes.
+//
+// Rows.  The heads that share a key head are rows of one tile: row r of a
+// 128-row query tile is head r % G of token r / G, floor(128 / G) tokens a tile,
+// so that K and V are read once for the whole group.  A TMA box with the head
+// dimension between d and the tokens lays the rows out that way.
+//
+// Work.  A unit is two query tiles (a pair) of one sequence, for every kv head;
+// units with more key tiles come first.  Where the units times kv heads are
+// fewer than two per SM, they are cut along the keys into pieces of equal
+// length; the piece count is the one whose rounds over the SMs, partial writes
+// and merge reads cost least (plan_kernel, from the lengths on the device).
+// A cut unit leaves fp32 partials (O, LSE), merged by the LSE rule at the end.
+//
+// CTA roles (384 threads, one CTA an SM): warp 0 loads (TMA; one lane per
+// page and 64-column half), warp 1 lane 0 issues the MMAs, warp 2 clears the
+// value rows past a sequence's last key, warps 4..7 and 8..11 do the softmax of
+// query tile 0 and 1 (thread = row = TMEM lane).  TMEM: S_0 [0,128), S_1
+// [128,256), O_0 [256,256+D), O_1 [384,384+D); P_t (bf16) replaces S_t.  The
+// MMA order per key tile j is P_0 V_j, S_0(j+1), P_1 V_j, S_1(j+1): each tile's
+// softmax runs under two products of the other.
+//
+// Pages.  A tile of 128 keys is 128 / page boxes of a page each (one for pages
+// of 128 and more).  A page past the length or one that does not exist is
+// loaded from a coordinate outside the tensor map, which fills zeros, and its
+// keys are masked by a word per tile that the loader leaves in a ring.  Rows of
+// the last page past the length may hold anything: keys there are masked, and
+// values are cleared in shared memory before the product (0 * NaN is NaN).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "paged.h"
+#include "paged_merge.cuh"
+#include "ptx.cuh"
+#include "tma_host.h"
+
+namespace lsx {
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;  // base 2: P <= 256 under a stale maximum
+constexpr int kOkRing = 8;                 // >= stages + 2 (see the loader)
+constexpr int kMinPiece = 4;               // key tiles
+constexpr int kPiecesPerSm = 4;            // at most, over all units and kv heads
+constexpr int kPlanThreads = 512;
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = (D == 128) ? 2 : 4;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kSub = D / 64;  // 64-column (128 B) boxes
+};
+
+template <int D>
+struct __align__(1024) Smem {
+  __nv_bfloat16 q[2][128 * D];
+  __nv_bfloat16 k[Cfg<D>::kStages][128 * D];
+  __nv_bfloat16 v[Cfg<D>::kStages][128 * D];
+  uint64_t q_full, q_empty, final_bar;
+  uint64_t v_tail, v_fixed;  // the tile with a sequence's last key is in; its dead rows are cleared
+  uint64_t k_full[Cfg<D>::kStages];
+  uint64_t v_full[Cfg<D>::kStages];
+  uint64_t k_empty[Cfg<D>::kStages];
+  uint64_t v_empty[Cfg<D>::kStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint32_t keys_ok[kOkRing];  // bit g: keys [16 g, 16 g + 16) of the tile exist
+  uint32_t tail_stage;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// What a CTA works on: tokens [tok0, tok0 + ntok) of sequence b (rows of up to
+// two tiles) against key tiles [j0, j0 + size); the first token's last visible
+// key is lim0 (causal; each next token sees one more) and there are len keys.
+struct __align__(16) Entry {
+  int32_t b, tok0, ntok, j0, size, len, lim0, slot;  // slot < 0: the whole row range
+};
+// A cut unit for the merge: pieces first, .., first + n - 1.
+struct __align__(16) CutUnit {
+  int32_t tok0, ntok, first, n;
+};
+struct Header {
+  int32_t n_entries, n_cut;
+};
+
+struct FwdParams {
+  PagedCache c;
+  int64_t Hkv;
+  int G, per, tpt;  // heads of a group; rows of a token; tokens of a tile
+  const Header* header;
+  const Entry* entries;  // NULL: the uniform pieces below (a shared prefix)
+  int32_t u_tokens, u_len, u_pieces, u_size;
+  float scale_log2;
+  lsx_tensor o, lse;
+  float* part_o;  // [slot][Hkv][256][D]
+  float* part_l;  // [slot][Hkv][256]
+  int* status;
+  uint64_t wait_ns;
+};
+
+struct Item {
+  Entry e;
+  int hk;
+  int n[2];  // key tiles of query tile t
+};
+
+__device__ __forceinline__ int64_t item_count(const FwdParams& p) {
+  const int64_t n = p.entries == nullptr
+                        ? static_cast<int64_t>((p.u_tokens + 2 * p.tpt - 1) / (2 * p.tpt)) * p.u_pieces
+                        : __ldcg(&p.header->n_entries);
+  return n * p.Hkv;
+}
+
+// Tokens of tile t of an entry.
+__device__ __forceinline__ int tile_tokens(const FwdParams& p, const Entry& e, int t) {
+  const int n = e.ntok - t * p.tpt;
+  return n < 0 ? 0 : (n > p.tpt ? p.tpt : n);
+}
+// Last visible key of token i of an entry (the queries of a shared prefix have
+// no order: all see all of it).
+__device__ __forceinline__ int last_key(const FwdParams& p, const Entry& e, int i) {
+  const int lim = p.entries == nullptr ? e.lim0 : e.lim0 + i;
+  return lim < e.len - 1 ? lim : e.len - 1;
+}
+
+// Item `it` of the list: entry rank, kv head.
+__device__ __forceinline__ Item get_item(const FwdParams& p, int64_t it, int64_t n_entries) {
+  Item x;
+  int64_t rank, hk;
+  banded_item(it, n_entries, p.Hkv, &rank, &hk);
+  x.hk = static_cast<int>(hk);
+  if (p.entries != nullptr) {
+    const int4* src = reinterpret_cast<const int4*>(p.entries + rank);
+    const int4 a = __ldcg(src), b = __ldcg(src + 1);  // (written by the launch before)
+    x.e = Entry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  } else {  // piece-major: the pairs of one key range run together
+    const int pairs = static_cast<int>(n_entries) / p.u_pieces;
+    const int piece = static_cast<int>(rank) / pairs, pair = static_cast<int>(rank) % pairs;
+    const int tok0 = pair * 2 * p.tpt, left = p.u_tokens - tok0;
+    x.e = Entry{0, tok0, left < 2 * p.tpt ? left : 2 * p.tpt, piece * p.u_size, p.u_size,
+                p.u_len, p.u_len - 1, pair * p.u_pieces + piece};
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int cnt = tile_tokens(p, x.e, t);
+    const int last = cnt > 0 ? last_key(p, x.e, t * p.tpt + cnt - 1) : -1;
+    const int n = (last >= 0 ? (last >> 7) + 1 : 0) - x.e.j0;
+    x.n[t] = n < 0 ? 0 : (n > x.e.size ? x.e.size : n);
+  }
+  return x;
+}
+
+// Position (within the entry's tiles) of the tile whose value rows past the
+// last key have to be cleared, -1 when there is none.
+__device__ __forceinline__ int tail_tile(const FwdParams& p, const Entry& e, int nkv) {
+  if ((e.len & ((1 << p.c.shift) - 1)) == 0) return -1;
+  const int j = (e.len >> 7) - e.j0;
+  return j >= 0 && j < nkv ? j : -1;
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) break;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+  using C = Cfg<D>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const WaitGuard guard{p.status, p.wait_ns, &sm.abort};
+
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.final_bar, 1);
+    mbar_init(&sm.v_tail, 1);
+    mbar_init(&sm.v_fixed, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_full[t], 128);
+      mbar_init(&sm.o_full[t], 1);
+    }
+    fence_barrier_init();
+    tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  const int64_t n_items = item_count(p);
+  const int64_t n_entries = n_items / p.Hkv;
+  const int64_t grid = gridDim.x, c = blockIdx.x;
+  // registers: 128 * 104 + 256 * 200 = 64,512 = 384 * 168
+  if (warp < 4) {
+    regs_dec<104>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- loader
+      uint32_t stage = 0, phase = 0, qe_phase = 0, count = 0;
+      const int boxes = p.c.shift >= 7 ? 1 : 128 >> p.c.shift;  // per 64-column half
+      const int rows = 128 / boxes;
+      const int box = lane % boxes, sub = lane / boxes;
+      const uint32_t q_bytes = 2 * C::kSub * p.per * p.tpt * 128;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(bar, parity, guard);
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+      };
+      for (int64_t r = 0;; ++r) {
+        const int64_t it = snake_item(c, r, grid);
+        if (it >= n_items) break;
+        const Item x = get_item(p, it, n_entries);
+        const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
+        // page of each 16-key group of a tile in lanes 0..7, a tile ahead
+        const int32_t* row = p.c.table + x.e.b * p.c.table_stride;
+        auto fetch = [&](int j) -> int32_t {
+          const int pos = (x.e.j0 + j) * 128 + lane * 16;
+          return j < nkv && lane < 8 && pos < x.e.len ? __ldg(row + (pos >> p.c.shift)) : -1;
+        };
+        int32_t next = fetch(0);
+        if (!wait_all(&sm.q_empty, qe_phase ^ 1)) break;
+        qe_phase ^= 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full, q_bytes);
+          for (int t = 0; t < 2; ++t)
+            for (int s = 0; s < C::kSub; ++s) {
+              const int tok = x.e.tok0 + t * p.tpt;
+              tma_load_4d(&sm.q[t][s * 128 * 64], &tm_q, &sm.q_full, s * 64, x.hk * p.G,
+                          p.entries != nullptr ? tok : 0, p.entries != nullptr ? 0 : tok);
+            }
+        }
+        bool ok = true;
+        for (int j = 0; j < nkv; ++j) {
+          const int32_t mine = next;
+          next = fetch(j + 1);
+          const int pos = (x.e.j0 + j) * 128;
+          const bool exists = mine >= 0 && mine < p.c.n_pages;
+          if (lane < 8 && !exists && pos + lane * 16 < x.e.len)
+            atomicCAS(p.status, 0, kStatusPage);
+          const uint32_t mask = __ballot_sync(0xffffffffu, exists) & 255u;
+          const int page =
+              __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * (8 / boxes)) & 7);
+          const int prow = p.c.shift > 7 ? pos & ((1 << p.c.shift) - 1) : 0;
+          if (!wait_all(&sm.k_empty[stage], phase ^ 1)) { ok = false; break; }
+          if (lane == 0) {
+            // (the word of 8 tiles ago: its readers are done, for the S product
+            // of the tile `stages` ago has been taken after their P)
+            *const_cast<volatile uint32_t*>(&sm.keys_ok[count % kOkRing]) = mask;
+            mbar_arrive_expect_tx(&sm.k_full[stage], C::kTileBytes);
+          }
+          __syncwarp();
+          if (lane < boxes * C::kSub)
+            tma_load_4d(&sm.k[stage][sub * 128 * 64 + box * rows * 64], &tm_k, &sm.k_full[stage],
+                        sub * 64, prow, x.hk, page);
+          if (!wait_all(&sm.v_empty[stage], phase ^ 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[stage], C::kTileBytes);
+          __syncwarp();
+          if (lane < boxes * C::kSub)
+            tma_load_4d(&sm.v[stage][sub * 128 * 64 + box * rows * 64], &tm_v, &sm.v_full[stage],
+                        sub * 64, prow, x.hk, page);
+          ++count;
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------ MMA issuer
+      constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, D, 0, 1);
+      // S_t(j+1) overwrites the columns of P_t(j); issued right after P_t(j) V_j
+      // by this thread, whose products execute in order.
+      uint32_t kst = 0, kph = 0, vst = 0, vph = 0, q_phase = 0, fix_phase = 0;
+      uint32_t p_phase[2] = {0, 0};
+      bool issued = false;
+      const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(sm.q[0]), 16, 1024),
+                                  sdesc_sw128(smem_addr(sm.q[1]), 16, 1024)};
+      auto issue_s = [&](int t, uint32_t k_addr) {
+        const uint64_t k0 = sdesc_sw128(k_addr, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + t * 128, q_desc[t] + kmajor_step(kk, 128), k0 + kmajor_step(kk, 128),
+                 kIdS, kk > 0 ? 1u : 0u);
+        mma_commit(&sm.s_full[t]);
+      };
+      for (int64_t r = 0;; ++r) {
+        const int64_t it = snake_item(c, r, grid);
+        if (it >= n_items) break;
+        const Item x = get_item(p, it, n_entries);
+        const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
+        const int tail = tail_tile(p, x.e, nkv);
+        if (!mbar_wait(&sm.q_full, q_phase, guard)) break;
+        q_phase ^= 1;
+        tc_fence_after();
+        bool ok = true;
+        if (nkv > 0) {  // S_t(0)
+          if (!mbar_wait(&sm.k_full[kst], kph, guard)) break;
+          tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (x.n[t] > 0) issue_s(t, smem_addr(sm.k[kst]));
+          issued = true;
+          mma_commit(&sm.k_empty[kst]);
+          if (++kst == kStages) { kst = 0; kph ^= 1; }
+        }
+        for (int j = 0; j < nkv; ++j) {
+          if (!mbar_wait(&sm.v_full[vst], vph, guard)) { ok = false; break; }
+          if (j == tail) {
+            sm.tail_stage = vst;
+            mbar_arrive(&sm.v_tail);
+            if (!mbar_wait(&sm.v_fixed, fix_phase, guard)) { ok = false; break; }
+            fix_phase ^= 1;
+          }
+          tc_fence_after();
+          const uint64_t v0 = sdesc_sw128(smem_addr(sm.v[vst]), 128 * 128, 1024);
+          const bool has_next = j + 1 < nkv;
+          bool k_ready = false;
+          for (int t = 0; t < 2; ++t) {
+            if (j < x.n[t]) {
+              if (!mbar_wait(&sm.p_full[t], p_phase[t], guard)) { ok = false; break; }
+              p_phase[t] ^= 1;
+              tc_fence_after();
+              const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v0 + mnmajor_step(kk), kIdO,
+                       kk > 0 ? 1u : acc0);
+              mma_commit(&sm.o_full[t]);
+            }
+            if (has_next && j + 1 < x.n[t]) {
+              if (!k_ready) {
+                if (!mbar_wait(&sm.k_full[kst], kph, guard)) { ok = false; break; }
+                tc_fence_after();
+                k_ready = true;
+              }
+              issue_s(t, smem_addr(sm.k[kst]));
+            }
+          }
+          if (!ok) break;
+          if (has_next) {
+            if (!k_ready) {
+              if (!mbar_wait(&sm.k_full[kst], kph, guard)) { ok = false; break; }
+            }
+            mma_commit(&sm.k_empty[kst]);
+            if (++kst == kStages) { kst = 0; kph ^= 1; }
+          }
+          mma_commit(&sm.v_empty[vst]);
+          if (++vst == kStages) { vst = 0; vph ^= 1; }
+        }
+        if (!ok) break;
+        mma_commit(&sm.q_empty);
+      }
+      if (issued) {  // every product has completed before TMEM is released
+        mma_commit(&sm.final_bar);
+        drain_wait(&sm.final_bar, 0, p.wait_ns);
+      }
+    } else if (warp == 2) {
+      // --------------------------------- value rows past the last key
+      // (when the MMA thread asks for it: it knows the stage, and waits)
+      uint32_t phase = 0;
+      for (int64_t r = 0;; ++r) {
+        const int64_t it = snake_item(c, r, grid);
+        if (it >= n_items) break;
+        const Item x = get_item(p, it, n_entries);
+        if (tail_tile(p, x.e, x.n[0] > x.n[1] ? x.n[0] : x.n[1]) >= 0) {
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait(&sm.v_tail, phase, guard);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          phase ^= 1;
+          const uint32_t st = *const_cast<volatile uint32_t*>(&sm.tail_stage);
+          // rows [len, end of its page) of the tile; pages after it are zeros
+          const int r0 = x.e.len & 127;
+          const int r1e = (x.e.len | ((1 << p.c.shift) - 1)) + 1 - (x.e.len & ~127);
+          const int r1 = r1e < 128 ? r1e : 128;
+          uint4* base = reinterpret_cast<uint4*>(sm.v[st]);
+          for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+            for (int s = 0; s < C::kSub; ++s) base[s * 128 * 8 + i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.v_fixed);
+        }
+      }
+    }
+  } else {
+    regs_inc<200>();
+    // ----------------------------------------------------------- softmax
+    const int t = (warp - 4) >> 2;
+    const int row = threadIdx.x - 128 * (1 + t);  // 0..127 == TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * 128;
+    const uint32_t tO = tS + 256;
+    uint32_t s_phase = 0, pv_count = 0, count = 0;
+    const float sl2 = p.scale_log2;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return mbar_wait(bar, parity, WaitGuard{p.status, p.wait_ns, &sm.abort});
+    };
+    for (int r = 0;; ++r) {
+      const int64_t it = snake_item(blockIdx.x, r, gridDim.x);
+      if (it >= n_items) break;
+      int nkv, kb, lim, lim_tile, tiles;
+      {
+        const Item x = get_item(p, it, n_entries);
+        nkv = x.n[t];
+        tiles = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
+        kb = x.e.j0 * 128;
+        lim = last_key(p, x.e, t * p.tpt + row / p.per);
+        lim_tile = last_key(p, x.e, t * p.tpt);
+      }
+      float m = kNegInf, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nkv; ++j, kb += 128) {
+        if (!wait(&sm.s_full[t], s_phase)) { ok = false; break; }
+        s_phase ^= 1;
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t u0[32], u1[32], u2[32], u3[32];
+          tmem_ld32(tS, u0);
+          tmem_ld32(tS + 32, u1);
+          tmem_ld32(tS + 64, u2);
+          tmem_ld32(tS + 96, u3);
+          tmem_ld_wait32(u0);
+          reg_fence32(u1);
+          reg_fence32(u2);
+          reg_fence32(u3);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(u0[i]);
+            s[32 + i] = __uint_as_float(u1[i]);
+            s[64 + i] = __uint_as_float(u2[i]);
+            s[96 + i] = __uint_as_float(u3[i]);
+          }
+        }
+        if (kb + 127 > lim_tile) {
+          const int last = lim - kb;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > last) s[i] = kNegInf;
+        }
+        const uint32_t okm = *const_cast<volatile uint32_t*>(&sm.keys_ok[(count + j) % kOkRing]);
+        if (okm != 255u) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (((okm >> (i / 16)) & 1u) == 0) s[i] = kNegInf;
+        }
+        float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+        for (int i = 4; i < 124; i += 8) {
+          mx0 = fmax3(mx0, s[i], s[i + 1]);
+          mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
+          mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
+          mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
+        }
+        mx0 = fmax3(mx0, s[124], s[125]);
+        mx1 = fmax3(mx1, s[126], s[127]);
+        const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+        const float m_new = fmaxf(m, mx * sl2);
+        if (j == 0) {
+          m = m_new;
+        } else {
+          const bool need = m_new > m + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, need)) {
+            // O_t must hold the finished P_t V of the previous key tile
+            if (!wait(&sm.o_full[t], (pv_count - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const float alpha = (m == kNegInf) ? 0.f : ex2(m - m_new);
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t u[32];
+              tmem_ld32(tO + cc * 32, u);
+              tmem_ld_wait32(u);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+              tmem_st32(tO + cc * 32, u);
+            }
+            tmem_st_wait();
+            l *= alpha;
+            m = m_new;
+          }
+        }
+        const float mu = (m == kNegInf) ? 0.f : m;
+        const float2 sc2 = make_float2(sl2, sl2);
+        const float2 nm2 = make_float2(-mu, -mu);
+        float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 arg =
+                __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
+            const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
+            if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
+            pk[i] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(tS + cc * 16, pk);
+        }
+        l += (la.x + la.y) + (lb.x + lb.y);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[t]);
+        ++pv_count;
+      }
+      if (!ok) break;
+      count += tiles;
+      // ------------------------------------------------------- epilogue
+      const Item x = get_item(p, it, n_entries);
+      const int tok = row / p.per, rem = row - tok * p.per;
+      const bool valid = tok < tile_tokens(p, x.e, t);
+      if (nkv > 0) {
+        if (!wait(&sm.o_full[t], (pv_count - 1) & 1)) break;
+        tc_fence_after();
+      }
+      const float inv = (l > 0.f) ? 1.f / l : 0.f;
+      const float lse = (l > 0.f) ? (m + lg2(l)) * kLn2 : kNegInf;
+      const bool part = x.e.slot >= 0;
+      const int64_t prow =
+          (static_cast<int64_t>(x.e.slot) * p.Hkv + x.hk) * 256 + t * 128 + row;
+      const int64_t token = x.e.tok0 + t * p.tpt + tok;
+      const int64_t h = static_cast<int64_t>(x.hk) * p.G + rem;  // (direct: rem is the head)
+      float* f32 = part ? p.part_o + prow * D
+                        : (p.o.dtype == LSX_F32
+                               ? static_cast<float*>(p.o.data) + view_off(p.o, 0, h, token)
+                               : nullptr);
+      __nv_bfloat16* b16 = static_cast<__nv_bfloat16*>(p.o.data) + view_off(p.o, 0, h, token);
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t u[32];
+        if (nkv > 0) {
+          tmem_ld32(tO + cc * 32, u);
+          tmem_ld_wait32(u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = 0u;
+        }
+        if (!valid) continue;
+        float ov[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) ov[i] = l > 0.f ? __uint_as_float(u[i]) * inv : 0.f;
+        if (f32 != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(f32 + cc * 32 + i) =
+                make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(b16 + cc * 32 + i) =
+                make_uint4(pack_bf16(ov[i], ov[i + 1]), pack_bf16(ov[i + 2], ov[i + 3]),
+                           pack_bf16(ov[i + 4], ov[i + 5]), pack_bf16(ov[i + 6], ov[i + 7]));
+        }
+      }
+      if (valid) {
+        if (part)
+          p.part_l[prow] = lse;
+        else
+          static_cast<float*>(p.lse.data)[view_off(p.lse, 0, h, token)] = lse;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- plan
+struct PlanParams {
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int batch;
+  int64_t n_tokens, cap;  // packed tokens; keys a table row can hold
+  int64_t Hkv;
+  int tpt, sm_count;
+  int max_entries, max_slots;  // room in the workspace (slots per kv head)
+  Header* header;
+  Entry* entries;
+  CutUnit* cut;
+  int* status;
+};
+
+struct Seq {
+  int32_t q0, n, len;
+};
+__device__ __forceinline__ Seq plan_seq(const PlanParams& p, int b) {
+  Seq s;
+  const int64_t T = p.n_tokens;
+  int64_t q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+  q0 = q0 < 0 ? 0 : (q0 > T ? T : q0);
+  q1 = q1 < q0 ? q0 : (q1 > T ? T : q1);
+  s.q0 = static_cast<int32_t>(q0);
+  s.n = static_cast<int32_t>(q1 - q0);
+  s.len = p.kv_lens[b] < 0 ? 0 : p.kv_lens[b];
+  return s;
+}
+
+// Key tiles of a pair whose last token is the i-th of its sequence.
+__device__ __forceinline__ int32_t pair_tiles(int64_t cap, const Seq& s, int32_t i) {
+  int64_t vis = static_cast<int64_t>(s.len) - s.n + i + 1;
+  if (vis > cap) vis = cap;
+  return vis > 0 ? static_cast<int32_t>((vis + 127) >> 7) : 0;
+}
+
+constexpr int kCutUnits = 512;  // pairs that the cutting handles (two per SM is below)
+constexpr int kBuckets = 64;
+
+// One block: the units of all sequences, whether and how to cut them, and the
+// list of work, longest pieces first.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
+  extern __shared__ int32_t start[];  // [batch + 1] first pair of each sequence
+  __shared__ int32_t wsum[kPlanThreads / 32];
+  __shared__ int32_t tiles[kCutUnits], slot0[kCutUnits];
+  __shared__ int32_t hist[kBuckets + 1];
+  __shared__ unsigned long long best;
+  __shared__ int32_t longest;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x, lane = t & 31;
+  if (t == 0) { longest = 0; best = ~0ull; }
+  if (t <= kBuckets) hist[t] = 0;
+  const int pair_tok = 2 * p.tpt;
+  // pairs of each sequence, exclusive sums
+  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = t * per < p.batch ? t * per : p.batch;
+  const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
+  int32_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = plan_seq(p, b);
+    start[b] = mine;
+    mine += (s.n + pair_tok - 1) / pair_tok;
+    if (s.len > p.cap && s.n > 0) atomicCAS(p.status, 0, kStatusPage);
+  }
+  int32_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) wsum[t >> 5] = inc;
+  __syncthreads();
+  int32_t before = inc - mine, n_pairs = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < (t >> 5)) before += wsum[w];
+    n_pairs += wsum[w];
+  }
+  for (int b = b0; b < b1; ++b) start[b] += before;
+  if (t == 0) start[p.batch] = n_pairs;
+  __syncthreads();
+  if (n_pairs > p.max_entries) n_pairs = p.max_entries;  // (cu_q not ascending)
+  auto unit = [&](int i, Seq& s, int32_t& first) -> int32_t {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= i) lo = mid; else hi = mid;
+    }
+    s = plan_seq(p, lo);
+    first = (i - start[lo]) * pair_tok;
+    return lo;
+  };
+  const bool may_cut = p.max_slots > 0 && n_pairs <= kCutUnits &&
+                       n_pairs * p.Hkv < 2 * static_cast<int64_t>(p.sm_count);
+  int32_t top = 0;
+  for (int i = t; i < n_pairs; i += kPlanThreads) {
+    Seq s;
+    int32_t first;
+    unit(i, s, first);
+    const int32_t last = (first + pair_tok < s.n ? first + pair_tok : s.n) - 1;
+    const int32_t n = pair_tiles(p.cap, s, last);
+    if (may_cut) tiles[i] = n;
+    top = n > top ? n : top;
+  }
+  if (top > 0) atomicMax(&longest, top);
+  __syncthreads();
+  int32_t piece = longest > 0 ? longest : 1;
+  if (may_cut && longest >= 2 * kMinPiece) {
+    // candidate k: the longest unit in k pieces.  Cost in key tiles: a CTA's
+    // rounds, each with a piece and an epilogue (1.5 tiles when it leaves
+    // partials), and the merge (54 pieces of 128 KB a tile's time, 3 to start)
+    const int k = t + 1;
+    const int32_t w = (longest + k - 1) / k;
+    if (k == 1 || w >= kMinPiece) {
+      int64_t n = 0;
+      for (int i = 0; i < n_pairs; ++i) n += tiles[i] > w ? (tiles[i] + w - 1) / w : 1;
+      if (k == 1 || n <= p.max_slots) {
+        const int64_t all = n * p.Hkv, rounds = (all + p.sm_count - 1) / p.sm_count;
+        const float cost = rounds * (w + (k > 1 ? 1.5f : 0.f)) + (k > 1 ? 3.f + all / 54.f : 0.f);
+        atomicMin(&best, (static_cast<unsigned long long>(cost * 16.f) << 32) |
+                             static_cast<unsigned>(w));
+      }
+    }
+    __syncthreads();
+    piece = static_cast<int32_t>(best & 0xffffffffu);
+  }
+  // pieces of each unit: equal, at most `piece` tiles
+  auto cut = [&](int32_t n, int32_t& size) -> int32_t {
+    const int32_t k = n > piece ? (n + piece - 1) / piece : 1;
+    size = (n + k - 1) / k;
+    return size > 0 ? (n + size - 1) / size : 1;
+  };
+  int32_t n_cut = 0, n_slots = 0;
+  if (may_cut && t < 32) {  // slots and list of the cut units
+    for (int base = 0; base < n_pairs; base += 32) {
+      const int i = base + lane;
+      int32_t size, k = i < n_pairs ? cut(tiles[i], size) : 0;
+      const int32_t need = k > 1 ? k : 0;
+      int32_t sum = need;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const uint32_t cuts = __ballot_sync(0xffffffffu, k > 1);
+      if (i < n_pairs) {
+        slot0[i] = k > 1 ? n_slots + sum - need : -1;
+        if (k > 1) {
+          Seq s;
+          int32_t first;
+          unit(i, s, first);
+          p.cut[n_cut + __popc(cuts & ((1u << lane) - 1u))] =
+              CutUnit{s.q0 + first, s.n - first < pair_tok ? s.n - first : pair_tok, slot0[i], k};
+        }
+      }
+      n_slots += __shfl_sync(0xffffffffu, sum, 31);
+      n_cut += __popc(cuts);
+    }
+  }
+  __syncthreads();
+  const int32_t widest = piece > 0 ? piece : 1;
+  auto bucket = [&](int32_t size) {  // 0: the longest
+    const int32_t x = static_cast<int32_t>(static_cast<int64_t>(size) * (kBuckets - 1) / widest);
+    return kBuckets - 1 - (x < kBuckets ? x : kBuckets - 1);
+  };
+  const int rounds = longest > piece ? (longest + piece - 1) / piece : 1;  // a unit's most pieces
+  auto each = [&](auto&& f) {  // piece-major
+    for (int j = 0; j < rounds; ++j)
+      for (int i = t; i < n_pairs; i += kPlanThreads) {
+        Seq s;
+        int32_t first, size;
+        const int b = unit(i, s, first);
+        const int32_t nt = s.n - first < pair_tok ? s.n - first : pair_tok;
+        const int32_t n = pair_tiles(p.cap, s, first + nt - 1);
+        const int32_t k = cut(n, size);
+        if (j >= k) continue;
+        const int32_t left = n - j * size;
+        f(i, j, k, b, s, first, nt, left < size ? left : size, size);
+      }
+  };
+  each([&](int, int, int, int, const Seq&, int32_t, int32_t, int32_t now, int32_t) {
+    atomicAdd(&hist[bucket(now) + 1], 1);
+  });
+  __syncthreads();
+  if (t < 32) {
+    int32_t a = hist[1 + 2 * lane], b = hist[2 + 2 * lane];
+    int32_t sum = a + b;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    hist[1 + 2 * lane] = sum - b;
+    hist[2 + 2 * lane] = sum;
+  }
+  __syncthreads();
+  const int32_t total = hist[kBuckets];
+  each([&](int i, int j, int k, int b, const Seq& s, int32_t first, int32_t nt, int32_t now,
+           int32_t size) {
+    const int32_t at = atomicAdd(&hist[bucket(now)], 1);
+    const int64_t len = s.len > p.cap ? p.cap : s.len;
+    if (at < p.max_entries)
+      p.entries[at] = Entry{b, s.q0 + first, nt, j * size, now, static_cast<int32_t>(len),
+                            s.len - s.n + first, k > 1 ? slot0[i] + j : -1};
+  });
+  if (t == 0) *p.header = Header{total < p.max_entries ? total : p.max_entries, n_cut};
+}
+
+// ------------------------------------------------------------------ merge
+struct FwdMergeParams {
+  const Header* header;
+  const CutUnit* cut;
+  int64_t Hkv;
+  int G, tpt;
+  const float* part_o;
+  const float* part_l;
+  lsx_tensor o, lse;
+};
+
+// One warp per row of a cut unit.
+template <int D>
+__global__ void __launch_bounds__(256) paged_fwd_merge_kernel(const FwdMergeParams p) {
+  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t rows = __ldcg(&p.header->n_cut) * p.Hkv * 256;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < rows;
+       i += step) {
+    const int row = static_cast<int>(i & 255);
+    const int64_t hk = (i >> 8) % p.Hkv;
+    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 8) / p.Hkv);
+    const CutUnit x{u.x, u.y, u.z, u.w};
+    const int r = row & 127, tok = r / p.G, t = row >> 7;
+    if (tok >= p.tpt || t * p.tpt + tok >= x.ntok) continue;
+    RowMerge<D> sum;
+    sum.take(p.part_o, p.part_l, x.n, lane, [&](int64_t c) {
+      return ((x.first + c) * p.Hkv + hk) * 256 + row;
+    });
+    sum.store(p.o, p.lse, 0, hk * p.G + (r - tok * p.G), x.tok0 + t * p.tpt + tok, lane);
+  }
+}
+
+// ------------------------------------------------------------------- host
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// bf16 map with dims (innermost first) {D, n1, n2, n3}, element strides, box
+// {64, b1, b2, b3}, 128-byte swizzle; elements outside read as zero.
+bool encode4(CUtensorMap* map, const void* base, int64_t D, const int64_t (&n)[3],
+             int64_t s1, int64_t s2, int64_t s3, uint32_t b1, uint32_t b2, uint32_t b3) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  // the stride of an extent-1 dimension is never used; give it a legal value
+  if (n[0] == 1) s1 = D;
+  if (n[1] == 1) s2 = s1 * n[0];
+  if (n[2] == 1) s3 = s2 * n[1];
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
+  cuuint64_t str[3] = {(cuuint64_t)(s1 * 2), (cuuint64_t)(s2 * 2), (cuuint64_t)(s3 * 2)};
+  cuuint32_t box[4] = {64u, b1, b2, b3};
+  cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, str, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_pages(CUtensorMap* map, const lsx_tensor& t) {
+  return encode4(map, t.data, t.D, {t.N, t.H, t.B}, t.stride_n, t.stride_h, t.stride_b,
+                 static_cast<uint32_t>(t.N < 128 ? t.N : 128), 1, 1);
+}
+
+template <int D>
+int launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                 const FwdParams& p, int64_t grid, bool early, cudaStream_t s) {
+  const size_t smem = sizeof(Smem<D>) + 1024;
+  if (cudaFuncSetAttribute(paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return LSX_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  timing_begin(kKidPagedFwd, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D>, tq, tk, tv, p);
+  timing_end(kKidPagedFwd, s);
+  return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
+}
+
+struct FwdLayout {
+  int64_t max_entries, max_slots;
+  size_t entries, cut, part_l, part_o, total;
+};
+FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, int64_t max_pages,
+                     int sm_count) {
+  FwdLayout x;
+  const int64_t G = q.H / kp.H, tpt = G <= 128 ? 128 / G : 1;
+  const int64_t tiles = ceil_div(max_pages * kp.N, 128);
+  x.max_slots = tiles >= 2 * kMinPiece ? kPiecesPerSm * sm_count / kp.H : 0;
+  if (x.max_slots < 2) x.max_slots = 0;
+  x.max_entries = ceil_div(q.N, 2 * tpt) + batch;
+  if (x.max_entries < x.max_slots) x.max_entries = x.max_slots;
+  x.entries = 256;
+  x.cut = x.entries + align256(static_cast<size_t>(x.max_entries) * sizeof(Entry));
+  x.part_l = x.cut + align256(kCutUnits * sizeof(CutUnit));
+  const size_t rows = static_cast<size_t>(x.max_slots * kp.H) * 256;
+  x.part_o = x.part_l + align256(rows * 4);
+  x.total = x.part_o + align256(rows * static_cast<size_t>(q.D) * 4);
+  return x;
+}
+
+}  // namespace
+
+size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
+                           int64_t max_pages, int sm_count) {
+  return fwd_layout(q, k_pages, batch, max_pages, sm_count).total;
+}
+
+int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
+                     const PagedCache& c, const int32_t* kv_lens, const int32_t* cu_q,
+                     int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse,
+                     void* workspace, const DeviceCtx& ctx, cudaStream_t s) {
+  const FwdLayout x = fwd_layout(q, k_pages, batch, c.max_pages, ctx.sm_count);
+  char* ws = static_cast<char*>(workspace);
+  FwdParams p;
+  p.c = c;
+  p.Hkv = k_pages.H;
+  p.G = static_cast<int>(q.H / k_pages.H);
+  p.per = p.G;
+  p.tpt = 128 / p.G;
+  p.header = reinterpret_cast<Header*>(ws);
+  p.entries = reinterpret_cast<Entry*>(ws + x.entries);
+  p.u_tokens = p.u_len = p.u_pieces = p.u_size = 0;
+  p.scale_log2 = scale * kLog2e;
+  p.o = o; p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws + x.part_o);
+  p.part_l = reinterpret_cast<float*>(ws + x.part_l);
+  p.status = ctx.status;
+  p.wait_ns = ctx.wait_ns;
+  CUtensorMap tq, tk, tv;
+  if (!encode4(&tq, q.data, q.D, {q.H, q.N, 1}, q.stride_h, q.stride_n, 0,
+               static_cast<uint32_t>(p.G), static_cast<uint32_t>(p.tpt), 1) ||
+      !encode_pages(&tk, k_pages) || !encode_pages(&tv, v_pages))
+    return LSX_ERR_LAUNCH;
+  PlanParams pp;
+  pp.kv_lens = kv_lens;
+  pp.cu_q = cu_q;
+  pp.batch = static_cast<int>(batch);
+  pp.n_tokens = q.N;
+  pp.cap = static_cast<int64_t>(c.max_pages) << c.shift;
+  pp.Hkv = p.Hkv;
+  pp.tpt = p.tpt;
+  pp.sm_count = ctx.sm_count;
+  pp.max_entries = static_cast<int>(x.max_entries);
+  pp.max_slots = static_cast<int>(x.max_slots);
+  pp.header = reinterpret_cast<Header*>(ws);
+  pp.entries = reinterpret_cast<Entry*>(ws + x.entries);
+  pp.cut = reinterpret_cast<CutUnit*>(ws + x.cut);
+  pp.status = ctx.status;
+  timing_begin(kKidPagedPlan, s);
+  paged_plan_kernel<<<1, kPlanThreads, (batch + 1) * sizeof(int32_t), s>>>(pp);
+  timing_end(kKidPagedPlan, s);
+  if (cudaGetLastError() != cudaSuccess) return LSX_ERR_LAUNCH;
+  const int64_t most = x.max_entries * p.Hkv;
+  const int64_t grid = most < ctx.sm_count ? most : ctx.sm_count;
+  const int rc = q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, true, s)
+                            : launch_tiles<64>(tq, tk, tv, p, grid, true, s);
+  if (rc != LSX_OK || x.max_slots == 0) return rc;
+  const FwdMergeParams mp{pp.header, pp.cut, p.Hkv, p.G, p.tpt, p.part_o, p.part_l, o, lse};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(4 * ctx.sm_count));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  timing_begin(kKidPagedMerge, s);
+  const cudaError_t e = q.D == 128 ? cudaLaunchKernelEx(&cfg, paged_fwd_merge_kernel<128>, mp)
+                                   : cudaLaunchKernelEx(&cfg, paged_fwd_merge_kernel<64>, mp);
+  timing_end(kKidPagedMerge, s);
+  return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
+}
+
+}  // namespace lsx
