@@ -79,13 +79,14 @@ SIGNATURES = {
     "attn_decode": (_INT, [_P, _P, _P, _I64, ctypes.c_float, _P, _P, _VP, _SZ, _VP]),
     "attn_page_map": (_INT, [_VP, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _VP,
                              _VP]),
-    "attn_page_append": (_INT, [_P, _P, _VP, _P, _P, _VP]),
-    "attn_paged_decode_workspace_size": (_SZ, [_P, _P, _I64, _I64]),
-    "attn_paged_decode": (_INT, [_P, _P, _P, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _P, _P,
-                                 _VP, _SZ, _VP]),
-    "attn_paged_fwd_workspace_size": (_SZ, [_P, _P, _I64, _I64]),
-    "attn_paged_fwd": (_INT, [_P, _P, _P, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _P, _P,
-                              _VP, _SZ, _VP]),
+    # (views as addresses: paged.py packs a call's views into one buffer)
+    "attn_page_append": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP]),
+    "attn_paged_decode_workspace_size": (_SZ, [_VP, _VP, _I64, _I64]),
+    "attn_paged_decode": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _VP,
+                                 _VP, _VP, _SZ, _VP]),
+    "attn_paged_fwd_workspace_size": (_SZ, [_VP, _VP, _I64, _I64]),
+    "attn_paged_fwd": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _I64, ctypes.c_float, _VP,
+                              _VP, _VP, _SZ, _VP]),
     "lsx_sync_status": (_INT, [_VP]),
     "lsx_status_string": (ctypes.c_char_p, [_INT]),
     "lsx_set_wait_limit_ns": (None, [ctypes.c_uint64]),

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace lsx {
@@ -47,6 +49,19 @@ inline PagedCache paged_cache(const lsx_tensor& kp, const lsx_tensor& vp, const 
   return c;
 }
 
+// Raises a kernel's dynamic shared memory limit, once per device (`done`: a
+// static of the kernel's launcher, a bit per device; setting it twice is
+// harmless).
+template <typename Kernel>
+inline bool allow_smem(Kernel kern, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 int launch_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch,
                     const int32_t* free_pages, int64_t n_free, int64_t page_size,
                     int32_t* block_table, int64_t table_stride, int64_t max_pages,
@@ -60,10 +75,23 @@ int launch_page_append(const lsx_tensor& k, const lsx_tensor& v, const int64_t* 
 // or the pages of prefix_len keys that every sequence sees first.
 size_t paged_decode_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t max_pages,
                               int64_t prefix_len, int sm_count);
-int launch_paged_decode(const lsx_tensor& q, const PagedCache& c, int64_t hkv,
-                        const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
+int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
+                        const PagedCache& c, const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
                         float scale, const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
                         const DeviceCtx& ctx, cudaStream_t s);
+// Partials of every decode query against a prefix that all of them see, on
+// the prompt kernel: piece i of the row that is token (b, n) of head g of kv head
+// hk is row ((b / (2 tpt) * pieces + i) * Hkv + hk) * 256 + (b / tpt % 2) * 128 +
+// ((b % tpt) * Nq + n) * G + g of o [rows][D] and l [rows].
+struct PrefixPlan {
+  int tpt, pieces, size;  // sequences of a row tile; pieces of the prefix, key tiles each
+  int64_t rows;           // of all pieces
+};
+PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, int sm_count);
+int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
+                  const PagedCache& prefix, int64_t prefix_len, const PrefixPlan& plan,
+                  float scale, float* part_o, float* part_l, const DeviceCtx& ctx,
+                  cudaStream_t s);
 // Ragged prompt tokens, causal, over the pages.
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
                            int64_t max_pages, int sm_count);

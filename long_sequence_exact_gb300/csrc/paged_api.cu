@@ -145,7 +145,7 @@ int attn_paged_decode(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_
   DeviceCtx ctx;
   LSX_TRY(device_ctx(&ctx));
   const PagedCache c = paged_cache(*k_pages, *v_pages, block_table, table_stride, max_pages);
-  return launch_paged_decode(*q, c, k_pages->H, kv_lens, prefix_table, prefix_len,
+  return launch_paged_decode(*q, *k_pages, *v_pages, c, kv_lens, prefix_table, prefix_len,
                              resolve_scale(scale, q->D), *o, *lse, workspace, ctx,
                              as_stream(stream));
 }

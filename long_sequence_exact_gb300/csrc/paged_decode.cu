@@ -16,18 +16,20 @@
 // runs, combines them by the LSE rule in the order of the keys.  Which run
 // holds what follows from the lengths alone, which every CTA sums for itself.
 //
-// A step: 128 threads copy 64 rows of K and V (cp.async, 16 bytes each, rows
-// past the length and of pages that do not exist zero-filled) into one of the
-// ring's stages, 96 KB an SM's half; the loads run ahead of the compute across
-// unit ends.  Scores and output by warp-level bf16 MMAs: 16 query rows (padded)
-// x 16 keys a time; the warps share the step's keys (and, from 17 rows on,
-// the row tiles).  P enters the P V product as the sum of two bf16, so that the
-// result keeps 16 bits of it: the tensor cores are idle otherwise.
+// A step is 16 KB of keys and 16 KB of values (64 keys of 128, 128 keys of 64),
+// loaded page by page with TMA into one of three stages by a warp of its own,
+// which runs ahead across unit ends; pages past the length and pages that do not
+// exist come from outside the tensor map and read as zeros.  Scores and output
+// by warp-level bf16 MMAs, 16 query rows (padded) x 16 keys a time; the four
+// compute warps share the step's keys (and, from 17 rows on, the row tiles).  P
+// enters the P V product as the sum of two bf16, so that the result keeps 16
+// bits of it: the tensor cores are idle otherwise.
 #include <math.h>
 
 #include "paged.h"
 #include "paged_merge.cuh"
 #include "ptx.cuh"
+#include "tma_host.h"
 
 namespace lsx {
 namespace {
@@ -35,8 +37,8 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 128;
-constexpr int kStep = 64;       // keys per step
+constexpr int kWarps = 4;                       // compute warps
+constexpr int kThreads = 32 * (kWarps + 1);     // and the loader
 constexpr int kCtasPerSm = 2;
 
 // Output rows of a call: global row gr = (b * G + g) * Nq + n within a kv head.
@@ -66,28 +68,18 @@ struct PagedDecodeParams {
   PartView part;
   int64_t* start;       // [units_b + 1] first step of each, per kv head
   int* status;
+  uint64_t wait_ns;
 };
 
 template <int D>
 struct DecodeCfg {
+  static constexpr int kStep = 8192 / D;               // keys per step
+  static constexpr int kSub = D / 64;                  // 64-column (128 B) boxes
   static constexpr int kTile = kStep * D * 2;          // bytes of K (or V) per stage
-  static constexpr int kStages = 96 * 1024 / (2 * kTile);
+  static constexpr int kStages = 3;
   static constexpr int kXfer = 2 * 16 * D * 4;         // two warps' O, for the join
-  static constexpr int kSmem = kStages * 2 * kTile + kXfer;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__host__ __device__ constexpr int step_keys(int64_t d) { return static_cast<int>(8192 / d); }
 
 // Keys of unit row b, clamped to what the table holds.
 __device__ __forceinline__ int32_t unit_len(const PagedDecodeParams& p, int64_t b) {
@@ -97,6 +89,7 @@ __device__ __forceinline__ int32_t unit_len(const PagedDecodeParams& p, int64_t 
   return n < 0 ? 0 : (n > cap ? static_cast<int32_t>(cap) : n);
 }
 // Steps of a unit: at least one, which writes the empty result.
+template <int kStep>
 __device__ __forceinline__ int32_t unit_steps(int32_t len) {
   return len > 0 ? (len + kStep - 1) / kStep : 1;
 }
@@ -107,6 +100,7 @@ struct Cursor {
   int hk;
   int32_t len, steps, step;
 };
+template <int kStep>
 __device__ __forceinline__ void advance(const PagedDecodeParams& p, Cursor& x) {
   if (++x.step < x.steps) return;
   x.step = 0;
@@ -114,12 +108,13 @@ __device__ __forceinline__ void advance(const PagedDecodeParams& p, Cursor& x) {
   x.hk = 0;
   if (++x.b < p.units_b) {
     x.len = unit_len(p, x.b);
-    x.steps = unit_steps(x.len);
+    x.steps = unit_steps<kStep>(x.len);
   }
 }
 
 // Sums the steps of all units and finds this block's run of them, steps
 // [t0, t1), and the unit that holds t0; block 0 writes the starts.
+template <int kStep>
 __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* sums, Cursor* place,
                                          int64_t& t0, int64_t& t1) {
   const int t = threadIdx.x;
@@ -127,7 +122,7 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
   const int64_t b0 = t * per < p.units_b ? t * per : p.units_b;
   const int64_t b1 = b0 + per < p.units_b ? b0 + per : p.units_b;
   int64_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += unit_steps(unit_len(p, b));
+  for (int64_t b = b0; b < b1; ++b) mine += unit_steps<kStep>(unit_len(p, b));
   int64_t inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -151,7 +146,7 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
   if (t0 >= before * h && t0 < (before + mine) * h) {
     int64_t at = before;
     for (int64_t b = b0; b < b1; ++b) {
-      const int32_t len = unit_len(p, b), n = unit_steps(len);
+      const int32_t len = unit_len(p, b), n = unit_steps<kStep>(len);
       if (t0 < (at + n) * h) {
         const int64_t r = t0 - at * h;
         *place = Cursor{b, static_cast<int>(r / n), len, n, static_cast<int32_t>(r % n)};
@@ -164,7 +159,7 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
     int64_t at = before;
     for (int64_t b = b0; b < b1; ++b) {
       p.start[b] = at;
-      at += unit_steps(unit_len(p, b));
+      at += unit_steps<kStep>(unit_len(p, b));
     }
     if (t == kThreads - 1) p.start[p.units_b] = total;
     if (p.lens != nullptr) {
@@ -176,90 +171,180 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
   __syncthreads();
 }
 
+// What a CTA keeps in shared memory behind the stages and the join's buffer.
+struct Shared {
+  int64_t sums[kThreads / 32];
+  Cursor place;
+  uint64_t full[3], empty[3];
+  uint32_t pages_ok[3];     // bit i: 16-key group i of the stage exists
+  int abort;
+  float xm[2][16], xl[2][16];  // the join's row maxima and sums
+};
+
+// Thread block clusters: this CTA's rank, a barrier over the cluster's threads
+// (their shared memory accesses ordered), and reads of a sibling's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t sibling(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+
+// The compute warps alone.
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+// Output row of unit row r, false when there is none.
+__device__ __forceinline__ bool out_row(const PagedDecodeParams& p, int64_t ub, int hk, int r,
+                                        int64_t& b, int64_t& h, int64_t& n) {
+  const int64_t gr = ub * p.R + r;
+  b = gr / p.rows.per;
+  if (r >= p.R || b >= p.rows.B) return false;
+  const int rem = static_cast<int>(gr - b * p.rows.per), g = rem / p.rows.Nq;
+  n = rem - g * p.rows.Nq;
+  h = static_cast<int64_t>(hk) * p.rows.G + g;
+  return true;
+}
+
 // RT: 16-row tiles of a unit (1, 2 or 4).  Warp w works on row tile w % RT and
 // on the keys [16 RT kg, +16 RT) of a step, kg = w / RT.
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
-    const PagedDecodeParams p) {
+// CL > 1: few short units.  A cluster of CL CTAs takes one unit, a CL-th of its
+// steps each, and joins the parts through its shared memory: no sums over the
+// lengths, no partials in memory, no second launch.
+template <int D, int RT, int CL>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedDecodeParams p) {
   using C = DecodeCfg<D>;
-  constexpr int kS = C::kStages, kPieces = D / 8, kRowsPerPass = kThreads / kPieces;
-  constexpr int kPasses = kStep / kRowsPerPass;
+  constexpr int kS = C::kStages, kStep = C::kStep;
+  constexpr int KB = RT * kStep / 64;  // 16-key blocks of a warp and step
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[kThreads / 32];
-  __shared__ Cursor place;
-  __shared__ uint32_t pages_ok[kS];          // bit i: 16-key group i exists
-  __shared__ float xm[2][16], xl[2][16];     // the join's row maxima and sums
+  float* const xo = reinterpret_cast<float*>(smem + kS * 2 * C::kTile);
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kS * 2 * C::kTile + C::kXfer);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rt = warp % RT, kg = warp / RT;
-  int64_t t0, t1;
-  find_run(p, sums, &place, t0, t1);
-  if (t0 >= t1) return;
-  const int n_steps = static_cast<int>(t1 - t0);
-
-  // ---- loads: the page numbers of a step's four 16-key groups, one per lane,
-  // are fetched a step ahead
-  Cursor ld = place;
-  int ld_left = n_steps;
-  auto fetch_page = [&]() -> int32_t {
-    if (ld_left <= 0 || lane >= 4) return -1;
-    const int32_t pos = ld.step * kStep + lane * 16;
-    if (pos >= ld.len) return -1;
-    return __ldg(p.c.table + ld.b * p.c.table_stride + (pos >> p.c.shift));
-  };
-  int32_t next_page = fetch_page();
-  const uint32_t smem0 = smem_addr(smem);
-  const int piece = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
-  auto issue = [&](int stage) {
-    if (ld_left > 0) {
-      const int32_t mine = next_page;
-      const Cursor x = ld;
-      advance(p, ld);
-      --ld_left;
-      next_page = fetch_page();
-      const bool ok = mine >= 0 && mine < p.c.n_pages;
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 15u;
-      if (threadIdx.x == 0) pages_ok[stage] = mask;
-      if (warp == 0 && lane < 4 && !ok && x.step * kStep + lane * 16 < x.len)
-        atomicCAS(p.status, 0, kStatusPage);
-      const uint32_t kd = smem0 + stage * 2 * C::kTile, vd = kd + C::kTile;
-      const int64_t k_h = x.hk * p.c.k_sh + piece * 8, v_h = x.hk * p.c.v_sh + piece * 8;
-      const int32_t in_page = (1 << p.c.shift) - 1;
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int r = row0 + i * kRowsPerPass;
-        const int32_t pos = x.step * kStep + r;
-        const int64_t page = __shfl_sync(0xffffffffu, ok ? mine : -1, r >> 4);
-        const bool live = pos < x.len && page >= 0;
-        const int64_t g = live ? page : 0, n = pos & in_page;
-        const uint32_t at = r * (D * 2) + ((piece ^ (r & 7)) << 4);
-        cp_async16(kd + at, p.c.k + g * p.c.k_sp + k_h + n * p.c.k_sn, live ? 16 : 0);
-        cp_async16(vd + at, p.c.v + g * p.c.v_sp + v_h + n * p.c.v_sn, live ? 16 : 0);
-      }
+  const WaitGuard guard{p.status, p.wait_ns, &sh.abort};
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kWarps);
     }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kS - 1; ++s) issue(s);
+    fence_barrier_init();
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
+  int64_t t0, t1;
+  const uint32_t rank = CL > 1 ? cluster_rank() : 0;
+  Cursor x;
+  if constexpr (CL > 1) {
+    const int64_t unit = blockIdx.x / CL;
+    x.b = unit / p.rows.Hkv;
+    x.hk = static_cast<int>(unit - x.b * p.rows.Hkv);
+    x.len = unit_len(p, x.b);
+    x.steps = unit_steps<kStep>(x.len);
+    t0 = static_cast<int64_t>(x.steps) * rank / CL;
+    t1 = static_cast<int64_t>(x.steps) * (rank + 1) / CL;
+    x.step = static_cast<int32_t>(t0);
+    if (threadIdx.x == 0 && rank == 0 &&
+        __ldg(p.lens + x.b) > static_cast<int64_t>(p.c.max_pages) << p.c.shift)
+      atomicCAS(p.status, 0, kStatusPage);
+    __syncthreads();  // the barriers
+  } else {
+    find_run<kStep>(p, sh.sums, &sh.place, t0, t1);
+    if (t0 >= t1) return;
+    x = sh.place;
+  }
+  const int n_steps = static_cast<int>(t1 - t0);
+  const uint32_t smem0 = smem_addr(smem);
 
-  // ---- compute
-  Cursor x = place;
-  bool whole = x.step == 0;  // the unit's keys so far are all in this run
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column
-  uint32_t qf[D / 16][4];
   float o[D / 8][4], m[2], l[2];
+  if (warp == kWarps) {
+    // ---- loader: the page numbers of a step's 16-key groups, one per lane, are
+    // fetched a step ahead; then one box per page, 64-column half and tensor
+    constexpr int kGroups = kStep / 16;
+    constexpr int kLog = kStep == 64 ? 6 : 7;
+    const int boxes = p.c.shift >= kLog ? 1 : kStep >> p.c.shift;
+    const int rows = kStep / boxes, per = kGroups / boxes;
+    const int box = lane % boxes, sub = lane / boxes % C::kSub, kv = lane / (boxes * C::kSub);
+    const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+    Cursor ld = x;
+    auto fetch = [&](int left) -> int32_t {
+      if (left <= 0 || lane >= kGroups) return -1;
+      const int32_t pos = ld.step * kStep + lane * 16;
+      return pos < ld.len ? __ldg(p.c.table + ld.b * p.c.table_stride + (pos >> p.c.shift)) : -1;
+    };
+    int32_t next = fetch(n_steps);
+    int issued = 0;
+    for (int it = 0; it < n_steps; ++it) {
+      const int32_t mine = next, pos = ld.step * kStep;
+      const int hk = ld.hk;
+      const bool exists = mine >= 0 && mine < p.c.n_pages;
+      if (lane < kGroups && !exists && pos + lane * 16 < ld.len)
+        atomicCAS(p.status, 0, kStatusPage);
+      advance<kStep>(p, ld);
+      next = fetch(n_steps - it - 1);
+      const uint32_t mask = __ballot_sync(0xffffffffu, exists);
+      const int page = __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * per) & 31);
+      const int stage = it % kS;
+      int ok = 1;
+      if (lane == 0) {
+        ok = it < kS || mbar_wait(&sh.empty[stage], ((it / kS) & 1) ^ 1, guard);
+        if (ok) {
+          sh.pages_ok[stage] = mask;
+          mbar_arrive_expect_tx(&sh.full[stage], 2 * C::kTile);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (kv < 2)
+        tma_load_4d(smem + (2 * stage + kv) * C::kTile + sub * kStep * 128 + box * rows * 128, map,
+                    &sh.full[stage], sub * 64, p.c.shift > kLog ? pos & ((1 << p.c.shift) - 1) : 0,
+                    hk, page);
+      ++issued;
+    }
+    if (issued < n_steps && lane == 0)  // gave up: wait for what is in flight
+      for (int i = issued > kS ? issued - kS : 0; i < issued; ++i) {
+        const uint64_t since = global_timer_ns();
+        while (!mbar_try_wait(&sh.full[i % kS], (i / kS) & 1))
+          if (global_timer_ns() - since > p.wait_ns) break;
+      }
+  }
+
+  // ---- compute (the loader's threads take part in the barriers only)
+  const bool computes = warp < kWarps;
+  bool whole = x.step == 0;  // the unit's keys so far are all in this run
+  uint32_t qf[D / 16][4];
   int32_t last[2];  // last visible key of rows qr, qr + 8 of the tile
   auto begin_unit = [&]() {
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      const int r = rt * 16 + qr + 8 * hh;
-      const int64_t gr = x.b * p.R + r;
-      const int64_t b = gr / p.rows.per;
-      const int rem = static_cast<int>(gr - b * p.rows.per), g = rem / p.rows.Nq,
-                n = rem - g * p.rows.Nq;
-      const bool live = r < p.R && b < p.rows.B;
-      const __nv_bfloat16* q =
-          p.q + b * p.q_sb + (static_cast<int64_t>(x.hk) * p.rows.G + g) * p.q_sh + n * p.q_sn;
+      int64_t b, h, n = 0;
+      const bool live = out_row(p, x.b, x.hk, rt * 16 + qr + 8 * hh, b, h, n);
+      const __nv_bfloat16* q = live ? p.q + b * p.q_sb + h * p.q_sh + n * p.q_sn : p.q;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[kk][hh] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kk * 16 + qc)) : 0u;
@@ -280,37 +365,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   };
-  begin_unit();
-  const uint32_t ld_row = (lane & 7), ld_mat = lane >> 3;
-  float* const xo = reinterpret_cast<float*>(smem + kS * 2 * C::kTile);
+  if (computes) begin_unit();
+  // ldmatrix rows of this lane: for K, 8 keys x 16 bytes of d per matrix, keys
+  // 8..15 in the upper two; for V (transposed), keys 8..15 in the odd ones.  A
+  // 128-byte line's 16-byte pieces are permuted by its address bits 7..9.
+  const uint32_t k_row = (lane & 7) + (lane >> 4) * 8, k_piece = (lane >> 3) & 1;
+  const uint32_t v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_piece = lane >> 4;
+  const uint32_t sw0 = smem0 >> 7;
 
-  for (int it = 0; it < n_steps; ++it) {
-    cp_async_wait<kS - 2>();
-    __syncthreads();
-    issue((it + kS - 1) % kS);
+  for (int it = 0; computes && it < n_steps; ++it) {
     const int stage = it % kS;
+    // (past a wait that ran out every wait returns at once: the run ends with
+    // the status set, all barriers met)
+    mbar_wait(&sh.full[stage], (it / kS) & 1, guard);
     const uint32_t kt = smem0 + stage * 2 * C::kTile, vt = kt + C::kTile;
-    const uint32_t ok_mask = pages_ok[stage];
-    // scores of 16 rows x 16 RT keys
-    float s[2 * RT][4];
+    const uint32_t ok_mask = *const_cast<volatile uint32_t*>(&sh.pages_ok[stage]);
+    // scores of 16 rows x 16 KB keys
+    float s[2 * KB][4];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const int key0 = (kg * RT + j) * 16;
+    for (int j = 0; j < KB; ++j) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[2 * j][e] = s[2 * j + 1][e] = 0.f;
-      const uint32_t r = key0 + ld_row + (ld_mat >> 1) * 8;
+      const uint32_t r = (kg * KB + j) * 16 + k_row;
+      const uint32_t line = kt + r * 128, sw = (sw0 + r) & 7;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t kb[4];
-        ldsm_x4(kt + r * (D * 2) + (((2 * kk + (ld_mat & 1)) ^ (r & 7)) << 4), kb);
+        ldsm_x4(line + (kk >> 2) * kStep * 128 + (((2 * (kk & 3) + k_piece) ^ sw) << 4), kb);
         mma_16816(s[2 * j], qf[kk], kb[0], kb[1]);
         mma_16816(s[2 * j + 1], qf[kk], kb[2], kb[3]);
       }
     }
     float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j) {
-      const int group = kg * RT + (j >> 1);
+    for (int j = 0; j < 2 * KB; ++j) {
+      const int group = kg * KB + (j >> 1);
       const bool ok = (ok_mask >> group) & 1u;
       const int32_t key = x.step * kStep + group * 16 + (j & 1) * 8 + qc;
 #pragma unroll
@@ -341,8 +430,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
       l[0] *= alpha[0];
       l[1] *= alpha[1];
     }
+    // rows of V past the last key may hold anything: cleared (0 * NaN is NaN)
+    const bool ragged = (x.step + 1) * kStep > x.len;
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
+    for (int j = 0; j < KB; ++j) {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -356,17 +447,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
           lo[2 * t + hh] = pack_bf16(a - __uint_as_float(h << 16),
                                      b - __uint_as_float(h & 0xffff0000u));
         }
-      const uint32_t r = (kg * RT + j) * 16 + ld_row + (ld_mat & 1) * 8;
+      const uint32_t r = (kg * KB + j) * 16 + v_row;
+      const uint32_t line = vt + r * 128, sw = (sw0 + r) & 7;
+      uint32_t keep[2] = {~0u, ~0u};
+      if (ragged) {
+        const int32_t left = x.len - (x.step * kStep + (kg * KB + j) * 16 + qc);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          keep[t] = (left > 8 * t ? 0xffffu : 0u) | (left > 8 * t + 1 ? 0xffff0000u : 0u);
+      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t vb[4];
-        ldsm_x4_t(vt + r * (D * 2) + (((2 * i + (ld_mat >> 1)) ^ (r & 7)) << 4), vb);
+        ldsm_x4_t(line + (i >> 2) * kStep * 128 + (((2 * (i & 3) + v_piece) ^ sw) << 4), vb);
+        if (ragged) {
+          vb[0] &= keep[0]; vb[1] &= keep[1];
+          vb[2] &= keep[0]; vb[3] &= keep[1];
+        }
         mma_16816(o[2 * i], hi, vb[0], vb[1]);
-        mma_16816(o[2 * i], lo, vb[0], vb[1]);
         mma_16816(o[2 * i + 1], hi, vb[2], vb[3]);
+        mma_16816(o[2 * i], lo, vb[0], vb[1]);
         mma_16816(o[2 * i + 1], lo, vb[2], vb[3]);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[stage]);
     const bool unit_end = x.step + 1 == x.steps;
     if (unit_end || it + 1 == n_steps) {
       // row sums over the four lanes of a row, then the join of the key groups
@@ -390,16 +495,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
           if ((lane & 3) == 0)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              xm[slot][qr + 8 * hh] = m[hh];
-              xl[slot][qr + 8 * hh] = l[hh];
+              sh.xm[slot][qr + 8 * hh] = m[hh];
+              sh.xl[slot][qr + 8 * hh] = l[hh];
             }
         }
-        __syncthreads();
+        compute_sync();
         if (kg < half) {
           float wa[2], wb[2];
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const float om = xm[slot][qr + 8 * hh], ol = xl[slot][qr + 8 * hh];
+            const float om = sh.xm[slot][qr + 8 * hh], ol = sh.xl[slot][qr + 8 * hh];
             const float m_new = fmaxf(m[hh], om);
             wa[hh] = m[hh] == kNegInf ? 0.f : ex2(m[hh] - m_new);
             wb[hh] = om == kNegInf ? 0.f : ex2(om - m_new);
@@ -416,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
               o[i][2 * hh + 1] = o[i][2 * hh + 1] * wa[hh] + y.y * wb[hh];
             }
         }
-        if (half > 1) __syncthreads();
+        compute_sync();  // (the buffer is free for the next round, or unit)
       }
+      if constexpr (CL > 1) break;  // (the cluster's one unit: joined below)
       if (kg == 0) {
         const bool direct = p.direct && whole && unit_end;
         // a cut unit: the run's first slot when it began in an earlier run, its
@@ -428,15 +534,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int r = rt * 16 + qr + 8 * hh;
-          const int64_t gr = x.b * p.R + r;
-          const int64_t b = gr / p.rows.per;
-          if (r >= p.R || b >= p.rows.B) continue;
+          int64_t b, h, n;
+          if (!out_row(p, x.b, x.hk, r, b, h, n)) continue;
           const float inv = l[hh] > 0.f ? 1.f / l[hh] : 0.f;
           const float lse = l[hh] > 0.f ? (m[hh] + lg2(l[hh])) * kLn2 : kNegInf;
           if (direct) {
-            const int rem = static_cast<int>(gr - b * p.rows.per), g = rem / p.rows.Nq,
-                      n = rem - g * p.rows.Nq;
-            const int64_t h = static_cast<int64_t>(x.hk) * p.rows.G + g;
             const int64_t at = view_off(p.o, b, h, n) + qc;
             if (p.o.dtype == LSX_F32) {
               float* dst = static_cast<float*>(p.o.data) + at;
@@ -463,11 +565,71 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_decode_kernel(
         }
       }
     }
-    advance(p, x);
+    advance<kStep>(p, x);
     if (unit_end) {
       whole = true;
       if (it + 1 < n_steps) begin_unit();
     }
+  }
+  if constexpr (CL > 1) {
+    // every CTA leaves its rows (sums over its keys) in its shared memory, and
+    // each takes every CL-th piece of four output elements from all of them
+    float* const part = reinterpret_cast<float*>(smem);  // [16 RT][D], stages now idle
+    float* const part_m = xo;
+    float* const part_l = xo + 16 * RT;
+    __syncthreads();
+    if (kg == 0 && computes) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = rt * 16 + qr + 8 * hh;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(part + r * D + i * 8 + qc) =
+              make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+        if ((lane & 3) == 0) {
+          part_m[r] = m[hh];
+          part_l[r] = l[hh];
+        }
+      }
+    }
+    cluster_sync();
+    for (int i = threadIdx.x * CL + rank; i < p.R * (D / 4); i += kThreads * CL) {
+      const int r = i / (D / 4), e = (i - r * (D / 4)) * 4;
+      float pm[CL], pl[CL];
+      float4 po[CL];
+#pragma unroll
+      for (int c = 0; c < CL; ++c) {
+        pm[c] = ld_cluster(sibling(smem_addr(part_m + r), c));
+        pl[c] = ld_cluster(sibling(smem_addr(part_l + r), c));
+        po[c] = ld_cluster4(sibling(smem_addr(part + r * D + e), c));
+      }
+      float mm = kNegInf, tot = 0.f;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) mm = fmaxf(mm, pm[c]);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < CL; ++c) {
+        const float w = pm[c] == kNegInf ? 0.f : ex2(pm[c] - mm);
+        tot += pl[c] * w;
+        s.x += po[c].x * w; s.y += po[c].y * w;
+        s.z += po[c].z * w; s.w += po[c].w * w;
+      }
+      const float inv = tot > 0.f ? 1.f / tot : 0.f;
+      int64_t b, h, n;
+      if (out_row(p, x.b, x.hk, r, b, h, n)) {
+        const int64_t at = view_off(p.o, b, h, n) + e;
+        if (p.o.dtype == LSX_F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.o.data) + at) =
+              make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o.data) + at) =
+              make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
+        if (e == 0)
+          static_cast<float*>(p.lse.data)[view_off(p.lse, b, h, n)] =
+              tot > 0.f ? (mm + lg2(tot)) * kLn2 : kNegInf;
+      }
+    }
+    cluster_sync();  // no CTA leaves while its rows are read
   }
 }
 
@@ -492,9 +654,17 @@ __device__ __forceinline__ void unit_runs(const RunView& v, int64_t b, int64_t h
   begins = a >= first * all / g;
 }
 
+// The prompt kernel's partials of a shared prefix (pieces 0: none).
+struct TileView {
+  int tpt, pieces;
+  const float* o;
+  const float* l;
+};
+
 struct PagedMergeParams {
   RowMap rows;
   RunView own, prefix;  // prefix.grid 0: none
+  TileView tiles;
   lsx_tensor o, lse;
 };
 
@@ -522,7 +692,14 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams
       return slot * v.R + r;
     });
   };
-  if (p.prefix.grid > 0) {
+  if (p.tiles.pieces > 0) {
+    const TileView& v = p.tiles;
+    const int64_t unit = b / (2 * v.tpt);
+    const int64_t at = (b / v.tpt % 2) * 128 +
+                       ((b % v.tpt) * p.rows.Nq + n) * p.rows.G + h % p.rows.G;
+    sum.take(v.o, v.l, v.pieces, lane,
+             [&](int64_t i) { return ((unit * v.pieces + i) * p.rows.Hkv + hk) * 256 + at; });
+  } else if (p.prefix.grid > 0) {
     take(p.prefix);
   } else {
     int64_t first, last;
@@ -550,61 +727,135 @@ RunLayout run_layout(int64_t slots, int64_t R, int64_t D, int64_t units, int64_t
   return x;
 }
 
-int64_t prefix_rows(int64_t rows) { return rows < kMaxDecodeRows ? rows : kMaxDecodeRows; }
+// More query rows than a warp kernel's CTA holds go to the prompt kernel.
+constexpr int64_t kMaxWarpRows = 32;
+
+struct PageMaps {
+  CUtensorMap k, v;
+};
+template <int D>
+constexpr int kSmem =
+    DecodeCfg<D>::kStages * 2 * DecodeCfg<D>::kTile + DecodeCfg<D>::kXfer + static_cast<int>(sizeof(Shared));
+// two CTAs, each with the system's 1 KB, on an SM's 228 KB
+static_assert(2 * (kSmem<128> + 1024) <= 228 * 1024, "shared memory of two CTAs");
+
+// Units a cluster each: all of them on the device at once, and short (the
+// table's width bounds the keys).  8 units of 128: 2048 keys 8.6 us, 13.6 us as
+// runs; 8192 keys 20.0 and 17.1 us; of 64: 8192 keys 10.0 and 13.5 us, 16384 keys
+// 15.7 and 15.1 us.
+constexpr int kCluster = 8;
+constexpr int64_t kClusterSteps = 12;  // of a CTA, at most
+bool fits_clusters(int64_t units, int64_t most_keys, int64_t d, int sm_count) {
+  return units * kCluster <= kCtasPerSm * static_cast<int64_t>(sm_count) &&
+         most_keys <= kCluster * kClusterSteps * step_keys(d);
+}
 
 template <int D, int RT>
-int launch_run(const PagedDecodeParams& p, int64_t grid, cudaStream_t s) {
-  auto kern = paged_decode_kernel<D, RT>;
-  constexpr int smem = DecodeCfg<D>::kSmem;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return LSX_ERR_LAUNCH;
+int launch_clusters(const PageMaps& maps, const PagedDecodeParams& p, int device, cudaStream_t s) {
+  auto kern = paged_decode_kernel<D, RT, kCluster>;
+  constexpr int smem = kSmem<D>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, smem, device, done)) return LSX_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.units_b * p.rows.Hkv * kCluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {kCluster, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   timing_begin(kKidPagedDecode, s);
-  kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, p);
+  timing_end(kKidPagedDecode, s);
+  return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
+}
+
+int launch_clusters(const PageMaps& maps, const PagedDecodeParams& p, int64_t d, int dev,
+                    cudaStream_t s) {
+  const int rt = p.R <= 16 ? 1 : (p.R <= 32 ? 2 : 4);
+  if (d == 128)
+    return rt == 1   ? launch_clusters<128, 1>(maps, p, dev, s)
+           : rt == 2 ? launch_clusters<128, 2>(maps, p, dev, s)
+                     : launch_clusters<128, 4>(maps, p, dev, s);
+  return rt == 1   ? launch_clusters<64, 1>(maps, p, dev, s)
+         : rt == 2 ? launch_clusters<64, 2>(maps, p, dev, s)
+                   : launch_clusters<64, 4>(maps, p, dev, s);
+}
+
+template <int D, int RT>
+int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t grid, int device,
+               cudaStream_t s) {
+  auto kern = paged_decode_kernel<D, RT, 1>;
+  constexpr int smem = kSmem<D>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, smem, device, done)) return LSX_ERR_LAUNCH;
+  timing_begin(kKidPagedDecode, s);
+  kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(maps.k, maps.v, p);
   timing_end(kKidPagedDecode, s);
   return cudaGetLastError() == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
 }
 
-int launch_run(const PagedDecodeParams& p, int64_t d, int64_t grid, cudaStream_t s) {
+int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t d, int64_t grid, int dev,
+               cudaStream_t s) {
   const int rt = p.R <= 16 ? 1 : (p.R <= 32 ? 2 : 4);
   if (d == 128)
-    return rt == 1 ? launch_run<128, 1>(p, grid, s)
-                   : (rt == 2 ? launch_run<128, 2>(p, grid, s) : launch_run<128, 4>(p, grid, s));
-  return rt == 1 ? launch_run<64, 1>(p, grid, s)
-                 : (rt == 2 ? launch_run<64, 2>(p, grid, s) : launch_run<64, 4>(p, grid, s));
+    return rt == 1   ? launch_run<128, 1>(maps, p, grid, dev, s)
+           : rt == 2 ? launch_run<128, 2>(maps, p, grid, dev, s)
+                     : launch_run<128, 4>(maps, p, grid, dev, s);
+  return rt == 1   ? launch_run<64, 1>(maps, p, grid, dev, s)
+         : rt == 2 ? launch_run<64, 2>(maps, p, grid, dev, s)
+                   : launch_run<64, 4>(maps, p, grid, dev, s);
 }
 
 }  // namespace
 
-size_t paged_decode_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t,
+size_t paged_decode_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t max_pages,
                               int64_t prefix_len, int sm_count) {
   const int64_t slots = 2 * kCtasPerSm * static_cast<int64_t>(sm_count);
   const int64_t per = q.H / k_pages.H * q.N;
+  if (prefix_len <= 0 && fits_clusters(q.B * k_pages.H, max_pages * k_pages.N, q.D, sm_count))
+    return 0;
   if (prefix_len <= 0) return run_layout(slots, per, q.D, q.B, 0).total;
-  const int64_t R = prefix_rows(q.B * per), groups = ceil_div(q.B * per, R);
-  return run_layout(slots, per, q.D, q.B, q.B * k_pages.H).total +
-         run_layout(slots, R, q.D, groups, groups * k_pages.H).total;
+  const size_t own = run_layout(slots, per, q.D, q.B, q.B * k_pages.H).total;
+  const int64_t R = q.B * per;
+  if (R <= kMaxWarpRows) return own + run_layout(slots, R, q.D, 1, k_pages.H).total;
+  const size_t rows = static_cast<size_t>(
+      prefix_plan(q.B, per, k_pages.H, prefix_len, sm_count).rows);
+  return own + align256(rows * 4) + align256(rows * static_cast<size_t>(q.D) * 4);
 }
 
-int launch_paged_decode(const lsx_tensor& q, const PagedCache& c, int64_t hkv,
-                        const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
+int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
+                        const PagedCache& c, const int32_t* kv_lens, const int32_t* prefix_table, int64_t prefix_len,
                         float scale, const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
                         const DeviceCtx& ctx, cudaStream_t s) {
   PagedDecodeParams p;
   p.c = c;
   p.q = static_cast<const __nv_bfloat16*>(q.data);
   p.q_sb = q.stride_b; p.q_sh = q.stride_h; p.q_sn = q.stride_n;
-  const int64_t per = q.H / hkv * q.N;
+  const int64_t hkv = k_pages.H, per = q.H / hkv * q.N;
   p.rows = RowMap{q.B, q.H, hkv, static_cast<int>(q.H / hkv), static_cast<int>(q.N),
                   static_cast<int>(per)};
   p.scale_log2 = scale * kLog2e;
   p.o = o; p.lse = lse;
   p.status = ctx.status;
+  p.wait_ns = ctx.wait_ns;
   const int64_t slots = 2 * kCtasPerSm * static_cast<int64_t>(ctx.sm_count);
   // at most one CTA per possible step
   auto runs = [&](int64_t units, int64_t most_keys) {
-    const int64_t steps = units * hkv * (most_keys > kStep ? ceil_div(most_keys, kStep) : 1);
+    const int64_t steps =
+        units * hkv * (most_keys > 0 ? ceil_div(most_keys, step_keys(q.D)) : 1);
     return steps < slots / 2 ? steps : slots / 2;
   };
+  const uint32_t box = static_cast<uint32_t>(
+      k_pages.N < step_keys(q.D) ? k_pages.N : step_keys(q.D));
+  PageMaps maps;
+  if (!make_map_bf16_4d(&maps.k, k_pages.data, k_pages.B, k_pages.H, k_pages.N, k_pages.D,
+                        k_pages.stride_b, k_pages.stride_h, k_pages.stride_n, box) ||
+      !make_map_bf16_4d(&maps.v, v_pages.data, v_pages.B, v_pages.H, v_pages.N, v_pages.D,
+                        v_pages.stride_b, v_pages.stride_h, v_pages.stride_n, box))
+    return LSX_ERR_LAUNCH;
   PagedMergeParams mp;
   mp.rows = p.rows; mp.o = o; mp.lse = lse;
   char* ws = static_cast<char*>(workspace);
@@ -619,26 +870,49 @@ int launch_paged_decode(const lsx_tensor& q, const PagedCache& c, int64_t hkv,
     return RunView{p.start, units, hkv, grid, slots, static_cast<int>(R), p.part};
   };
   mp.prefix = RunView{};
+  mp.tiles = TileView{};
   if (prefix_len > 0) {
-    const int64_t R = prefix_rows(q.B * per), units = ceil_div(q.B * per, R);
-    const int64_t grid = runs(units, prefix_len);
-    mp.prefix = place(R, units, grid);
     p.c.table = prefix_table;
     p.c.table_stride = 0;
     p.c.max_pages = static_cast<int32_t>(ceil_div(prefix_len, int64_t{1} << c.shift));
-    p.lens = nullptr;
-    p.fixed_len = prefix_len;
-    p.direct = 0;
-    const int rc = launch_run(p, q.D, grid, s);
+    int rc;
+    if (q.B * per <= kMaxWarpRows) {
+      const int64_t grid = runs(1, prefix_len);
+      mp.prefix = place(q.B * per, 1, grid);
+      p.lens = nullptr;
+      p.fixed_len = prefix_len;
+      p.direct = 0;
+      rc = launch_run(maps, p, q.D, grid, ctx.device, s);
+    } else {
+      const PrefixPlan plan = prefix_plan(q.B, per, hkv, prefix_len, ctx.sm_count);
+      float* part_l = reinterpret_cast<float*>(ws);
+      ws += align256(static_cast<size_t>(plan.rows) * 4);
+      float* part_o = reinterpret_cast<float*>(ws);
+      ws += align256(static_cast<size_t>(plan.rows * q.D) * 4);
+      mp.tiles = TileView{plan.tpt, plan.pieces, part_o, part_l};
+      rc = launch_prefix(q, k_pages, v_pages, p.c, prefix_len, plan, scale, part_o, part_l, ctx, s);
+    }
     if (rc != LSX_OK) return rc;
     p.c = c;
   }
-  const int64_t grid = runs(q.B, static_cast<int64_t>(c.max_pages) << c.shift);
+  const int64_t most_keys = static_cast<int64_t>(c.max_pages) << c.shift;
+  if (prefix_len == 0 && fits_clusters(q.B * hkv, most_keys, q.D, ctx.sm_count)) {
+    p.lens = kv_lens;
+    p.fixed_len = 0;
+    p.units_b = q.B;
+    p.R = static_cast<int>(per);
+    p.direct = 1;
+    p.start = nullptr;
+    p.part = PartView{};
+    p.whole_slot0 = 0;
+    return launch_clusters(maps, p, q.D, ctx.device, s);
+  }
+  const int64_t grid = runs(q.B, most_keys);
   mp.own = place(per, q.B, grid);
   p.lens = kv_lens;
   p.fixed_len = 0;
   p.direct = prefix_len > 0 ? 0 : 1;
-  const int rc = launch_run(p, q.D, grid, s);
+  const int rc = launch_run(maps, p, q.D, grid, ctx.device, s);
   if (rc != LSX_OK) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(q.B * q.H * q.N, 8)));

@@ -719,6 +719,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
       for (int i = 0; i < n_pairs; ++i) n += tiles[i] > w ? (tiles[i] + w - 1) / w : 1;
       if (k == 1 || n <= p.max_slots) {
         const int64_t all = n * p.Hkv, rounds = (all + p.sm_count - 1) / p.sm_count;
+        // (as cut_cost; an uncut unit writes its result itself)
         const float cost = rounds * (w + (k > 1 ? 1.5f : 0.f)) + (k > 1 ? 3.f + all / 54.f : 0.f);
         atomicMin(&best, (static_cast<unsigned long long>(cost * 16.f) << 32) |
                              static_cast<unsigned>(w));
@@ -872,11 +873,10 @@ bool encode_pages(CUtensorMap* map, const lsx_tensor& t) {
 
 template <int D>
 int launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                 const FwdParams& p, int64_t grid, bool early, cudaStream_t s) {
+                 const FwdParams& p, int64_t grid, bool early, int device, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + 1024;
-  if (cudaFuncSetAttribute(paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return LSX_ERR_LAUNCH;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(paged_fwd_kernel<D>, static_cast<int>(smem), device, done)) return LSX_ERR_LAUNCH;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(384);
@@ -915,7 +915,69 @@ FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, i
   return x;
 }
 
+// The cost, in the time of a key tile, of `units` units of `tiles` key tiles per
+// kv head cut into k pieces that leave partials: rounds over the SMs, each a piece and an
+// epilogue that writes 256 fp32 rows (1.5 tiles), and the merge, which reads
+// 54 such pieces of 128 KB in a tile's time.
+float cut_cost(int64_t units, int64_t tiles, int64_t k, int64_t hkv, int sm_count) {
+  const int64_t all = units * hkv * k;
+  return static_cast<float>(ceil_div(all, sm_count)) * (ceil_div(tiles, k) + 1.5f) + all / 54.f;
+}
+
 }  // namespace
+
+PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, int sm_count) {
+  PrefixPlan x;
+  // few sequences: both row tiles get half of them, so that each one's softmax
+  // runs under the other's products
+  x.tpt = static_cast<int>(128 / per);
+  if (B < 2 * x.tpt) x.tpt = static_cast<int>(ceil_div(B, 2));
+  const int64_t units = ceil_div(B, 2 * x.tpt), tiles = ceil_div(prefix_len, 128);
+  int64_t best = 1;
+  for (int64_t k = 2; units * hkv * k <= kPiecesPerSm * sm_count && ceil_div(tiles, k) >= kMinPiece;
+       ++k)
+    if (cut_cost(units, tiles, k, hkv, sm_count) < cut_cost(units, tiles, best, hkv, sm_count))
+      best = k;
+  x.size = static_cast<int>(ceil_div(tiles, best));
+  x.pieces = static_cast<int>(ceil_div(tiles, x.size));
+  x.rows = units * x.pieces * hkv * 256;
+  return x;
+}
+
+int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
+                  const PagedCache& prefix, int64_t prefix_len, const PrefixPlan& plan,
+                  float scale, float* part_o, float* part_l, const DeviceCtx& ctx,
+                  cudaStream_t s) {
+  FwdParams p;
+  p.c = prefix;
+  p.Hkv = k_pages.H;
+  p.G = static_cast<int>(q.H / k_pages.H);
+  p.per = static_cast<int>(p.G * q.N);
+  p.tpt = plan.tpt;
+  p.header = nullptr;
+  p.entries = nullptr;
+  p.u_tokens = static_cast<int32_t>(q.B);
+  p.u_len = static_cast<int32_t>(prefix_len);
+  p.u_pieces = plan.pieces;
+  p.u_size = plan.size;
+  p.scale_log2 = scale * kLog2e;
+  p.o = q;  // (not written: every row goes to the partials)
+  p.lse = q;
+  p.part_o = part_o;
+  p.part_l = part_l;
+  p.status = ctx.status;
+  p.wait_ns = ctx.wait_ns;
+  CUtensorMap tq, tk, tv;
+  if (!encode4(&tq, q.data, q.D, {q.H, q.N, q.B}, q.stride_h, q.stride_n, q.stride_b,
+               static_cast<uint32_t>(p.G), static_cast<uint32_t>(q.N),
+               static_cast<uint32_t>(p.tpt)) ||
+      !encode_pages(&tk, k_pages) || !encode_pages(&tv, v_pages))
+    return LSX_ERR_LAUNCH;
+  const int64_t items = plan.rows / 256;
+  const int64_t grid = items < ctx.sm_count ? items : ctx.sm_count;
+  return q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, false, ctx.device, s)
+                    : launch_tiles<64>(tq, tk, tv, p, grid, false, ctx.device, s);
+}
 
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
                            int64_t max_pages, int sm_count) {
@@ -969,8 +1031,8 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   if (cudaGetLastError() != cudaSuccess) return LSX_ERR_LAUNCH;
   const int64_t most = x.max_entries * p.Hkv;
   const int64_t grid = most < ctx.sm_count ? most : ctx.sm_count;
-  const int rc = q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, true, s)
-                            : launch_tiles<64>(tq, tk, tv, p, grid, true, s);
+  const int rc = q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, true, ctx.device, s)
+                            : launch_tiles<64>(tq, tk, tv, p, grid, true, ctx.device, s);
   if (rc != LSX_OK || x.max_slots == 0) return rc;
   const FwdMergeParams mp{pp.header, pp.cut, p.Hkv, p.G, p.tpt, p.part_o, p.part_l, o, lse};
   cudaLaunchConfig_t cfg{};

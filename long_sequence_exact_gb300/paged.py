@@ -24,24 +24,80 @@ length outside the cache is skipped on the device and reported by
 
 from __future__ import annotations
 
-from ctypes import byref
+import ctypes
+import struct
+import threading
 
 import torch
 
-from ._lib import check, load, stream_handle, view
+from . import _lib
+from ._lib import LSX_BF16, LSX_F32, LsxTensor, check, load
 
-_I32, _I64 = torch.int32, torch.int64
+_I32, _I64, _F32, _BF16, _U8 = (torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8)
+
+# One decode step is a call per layer: the views of a call are packed with one
+# struct.pack_into into a buffer of the calling thread, which the library reads
+# before it returns (a ctypes structure per view costs the call several
+# microseconds more).
+_VIEW = struct.calcsize("Pii7q")
+assert _VIEW == ctypes.sizeof(LsxTensor)
+_PACK = {n: struct.Struct("Pii7q" * n) for n in (2, 4, 5)}
 
 
-def _on_device(*tensors):
+class _Views(threading.local):
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(_VIEW * max(_PACK))
+        self.at = ctypes.addressof(self.buf)
+
+
+_views = _Views()
+
+
+def _pack(*tensors):
+    """Addresses of the lsx_tensor views of [B, H, N, D] tensors (D contiguous)
+    or [B, H, N] ones (an LSE), valid until the thread's next _pack."""
+    fields = []
+    for t in tensors:
+        dt = t.dtype
+        if dt is not _BF16 and dt is not _F32:
+            raise TypeError(f"unsupported dtype {dt}")
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 4:
+            b, h, n, d = shape
+            sb, sh, sn, sd = stride
+            if sd != 1 and d > 1:
+                raise ValueError("the last dimension must be contiguous")
+        elif len(shape) == 3:
+            b, h, n = shape
+            sb, sh, sn = stride
+            d = 1
+        else:
+            raise ValueError("expected a [B, H, N, D] or [B, H, N] tensor")
+        fields += (t.data_ptr(), LSX_BF16 if dt is _BF16 else LSX_F32, 0, b, h, n, d, sb, sh, sn)
+    views = _views
+    _PACK[len(tensors)].pack_into(views.buf, 0, *fields)
+    return range(views.at, views.at + _VIEW * len(tensors), _VIEW)
+
+
+def _device(*tensors):
+    """The current device, on which every tensor has to be."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"every tensor must be on the current CUDA device ({dev})")
+    return dev
+
+
+def _stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _stream = torch._C._cuda_getCurrentRawStream  # noqa: F811  (the same handle, without a Stream object)
 
 
 def _ints(t, name, n=None, dtype=_I32):
-    """A contiguous int vector (of n entries, when given)."""
+    """Pointer of a contiguous int vector (of n entries, when given)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.dim() != 1 or (n is not None and t.shape[0] != n):
@@ -63,6 +119,23 @@ def _table(t, batch):
     return t.data_ptr(), (t.stride(0) if batch > 1 else n), n
 
 
+def _outputs(q, out, lse, out_dtype):
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
+    return out, lse
+
+
+def _workspace(given, need, q):
+    """(tensor or None, pointer, bytes)"""
+    if given is None:
+        if need == 0:
+            return None, None, 0
+        given = torch.empty(need, dtype=_U8, device=q.device)
+    return given, given.data_ptr(), given.numel()
+
+
 def page_map(block_table, ctx_lens, new_lens, free_pages, page_size, n_tokens):
     """Pages and slots of one step's new tokens, from the request lengths.
 
@@ -74,8 +147,8 @@ def page_map(block_table, ctx_lens, new_lens, free_pages, page_size, n_tokens):
     and where there is no page), the first token of each sequence, the lengths
     with the new tokens, and the number of pages asked for (compare it with
     len(free_pages))."""
-    lib = load()
-    _on_device(block_table, ctx_lens, new_lens, free_pages)
+    lib = _lib._lib or load()
+    dev = _device(block_table, ctx_lens, new_lens, free_pages)
     if ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be a vector")
     batch, n_tokens = ctx_lens.shape[0], int(n_tokens)
@@ -84,23 +157,24 @@ def page_map(block_table, ctx_lens, new_lens, free_pages, page_size, n_tokens):
     table, stride, width = _table(block_table, batch)
     ctx, new, free = (_ints(ctx_lens, "ctx_lens"), _ints(new_lens, "new_lens", batch),
                       _ints(free_pages, "free_pages"))
-    slots = block_table.new_empty(n_tokens, dtype=_I64)
-    cu, lens, taken = ctx_lens.new_empty(2 * batch + 2).split((batch + 1, batch, 1))
+    slots = torch.empty(n_tokens, dtype=_I64, device=ctx_lens.device)
+    cu = torch.empty(batch + 1, dtype=_I32, device=ctx_lens.device)
+    lens = torch.empty_like(ctx_lens)
+    taken = torch.empty(1, dtype=_I32, device=ctx_lens.device)
     check(lib.attn_page_map(ctx, new, batch, free, free_pages.shape[0], int(page_size), table,
                             stride, width, slots.data_ptr(), n_tokens, cu.data_ptr(),
-                            lens.data_ptr(), taken.data_ptr(), stream_handle()), "attn_page_map")
+                            lens.data_ptr(), taken.data_ptr(), _stream(dev)), "attn_page_map")
     return slots, cu, lens, taken
 
 
 def page_append(k, v, k_pages, v_pages, slot_map):
     """Writes rows k, v [1, Hkv, T, D] (bf16, or f32 rounded once) into the slots
     slot_map int64 [T] of the pages; slots < 0 are skipped, the others distinct."""
-    lib = load()
-    _on_device(k, v, k_pages, v_pages, slot_map)
-    vk, vv, kp, vp = view(k), view(v), view(k_pages), view(v_pages)
+    lib = _lib._lib or load()
+    dev = _device(k, v, k_pages, v_pages, slot_map)
     slots = _ints(slot_map, "slot_map", k.shape[2], _I64)
-    check(lib.attn_page_append(byref(vk), byref(vv), slots, byref(kp), byref(vp),
-                               stream_handle()), "attn_page_append")
+    vk, vv, kp, vp = _pack(k, v, k_pages, v_pages)
+    check(lib.attn_page_append(vk, vv, slots, kp, vp, _stream(dev)), "attn_page_append")
 
 
 def paged_decode(q, k_pages, v_pages, block_table, kv_lens, scale=None, prefix_table=None,
@@ -109,13 +183,10 @@ def paged_decode(q, k_pages, v_pages, block_table, kv_lens, scale=None, prefix_t
     tokens of each sequence, (Hq / Hkv) * Nq <= 64.  With prefix_table (int32
     page numbers) every query sees prefix_len keys before its own, read once
     for many sequences together.  Returns (O, LSE)."""
-    lib = load()
-    b, h, n, d = q.shape
-    _on_device(q, k_pages, v_pages, block_table, kv_lens, prefix_table, out, lse, workspace)
-    if out is None:
-        out = q.new_empty((b, h, n, d), dtype=out_dtype or q.dtype)
-    if lse is None:
-        lse = q.new_empty((b, h, n), dtype=torch.float32)
+    lib = _lib._lib or load()
+    dev = _device(q, k_pages, v_pages, block_table, kv_lens, prefix_table, out, lse, workspace)
+    out, lse = _outputs(q, out, lse, out_dtype)
+    b = q.shape[0]
     table, stride, width = _table(block_table, b)
     lens = _ints(kv_lens, "kv_lens", b)
     prefix_len, prefix = int(prefix_len), None
@@ -123,21 +194,18 @@ def paged_decode(q, k_pages, v_pages, block_table, kv_lens, scale=None, prefix_t
         if prefix_table is None or prefix_table.shape[0] * k_pages.shape[2] < prefix_len:
             raise ValueError(f"prefix_table does not hold {prefix_len} keys")
         prefix = _ints(prefix_table, "prefix_table")
-    vq, kp, vp, vo, vl = view(q), view(k_pages), view(v_pages), view(out), view(lse)
-    if workspace is None:
-        workspace = q.new_empty(lib.attn_paged_decode_workspace_size(
-            byref(vq), byref(kp), width, prefix_len), dtype=torch.uint8)
-    check(lib.attn_paged_decode(byref(vq), byref(kp), byref(vp), table, stride, width, lens,
-                                prefix, prefix_len, -1.0 if scale is None else float(scale),
-                                byref(vo), byref(vl), workspace.data_ptr(), workspace.numel(),
-                                stream_handle()), "attn_paged_decode")
+    vq, kp, vp, vo, vl = _pack(q, k_pages, v_pages, out, lse)
+    ws, at, have = _workspace(
+        workspace, lib.attn_paged_decode_workspace_size(vq, kp, width, prefix_len), q)
+    check(lib.attn_paged_decode(vq, kp, vp, table, stride, width, lens, prefix, prefix_len,
+                                -1.0 if scale is None else float(scale), vo, vl, at, have,
+                                _stream(dev)), "attn_paged_decode")
     return out, lse
 
 
 def paged_decode_workspace_size(q, k_pages, max_pages, prefix_len=0) -> int:
-    vq, kp = view(q), view(k_pages)
-    return int(load().attn_paged_decode_workspace_size(byref(vq), byref(kp), int(max_pages),
-                                                       int(prefix_len)))
+    vq, kp = _pack(q, k_pages)
+    return int(load().attn_paged_decode_workspace_size(vq, kp, int(max_pages), int(prefix_len)))
 
 
 def paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q, scale=None, out=None, lse=None,
@@ -146,28 +214,21 @@ def paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q, scale=None, out=N
     sequence, those of sequence b at [cu_q[b], cu_q[b + 1]) (int32 [B + 1]), the
     last tokens of its kv_lens[b].  Returns (O, LSE) of the packed tokens; rows
     of no sequence are not written."""
-    lib = load()
-    b, h, n, d = q.shape
-    _on_device(q, k_pages, v_pages, block_table, kv_lens, cu_q, out, lse, workspace)
-    if out is None:
-        out = q.new_empty((b, h, n, d), dtype=out_dtype or q.dtype)
-    if lse is None:
-        lse = q.new_empty((b, h, n), dtype=torch.float32)
+    lib = _lib._lib or load()
+    dev = _device(q, k_pages, v_pages, block_table, kv_lens, cu_q, out, lse, workspace)
+    out, lse = _outputs(q, out, lse, out_dtype)
     batch = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
     table, stride, width = _table(block_table, batch)
     lens, cu = _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q", batch + 1)
-    vq, kp, vp, vo, vl = view(q), view(k_pages), view(v_pages), view(out), view(lse)
-    if workspace is None:
-        workspace = q.new_empty(lib.attn_paged_fwd_workspace_size(
-            byref(vq), byref(kp), batch, width), dtype=torch.uint8)
-    check(lib.attn_paged_fwd(byref(vq), byref(kp), byref(vp), table, stride, width, lens, cu,
-                             batch, -1.0 if scale is None else float(scale), byref(vo), byref(vl),
-                             workspace.data_ptr(), workspace.numel(), stream_handle()),
-          "attn_paged_fwd")
+    vq, kp, vp, vo, vl = _pack(q, k_pages, v_pages, out, lse)
+    ws, at, have = _workspace(
+        workspace, lib.attn_paged_fwd_workspace_size(vq, kp, batch, width), q)
+    check(lib.attn_paged_fwd(vq, kp, vp, table, stride, width, lens, cu, batch,
+                             -1.0 if scale is None else float(scale), vo, vl, at, have,
+                             _stream(dev)), "attn_paged_fwd")
     return out, lse
 
 
 def paged_fwd_workspace_size(q, k_pages, batch, max_pages) -> int:
-    vq, kp = view(q), view(k_pages)
-    return int(load().attn_paged_fwd_workspace_size(byref(vq), byref(kp), int(batch),
-                                                    int(max_pages)))
+    vq, kp = _pack(q, k_pages)
+    return int(load().attn_paged_fwd_workspace_size(vq, kp, int(batch), int(max_pages)))

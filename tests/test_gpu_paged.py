@@ -173,9 +173,10 @@ def decode_case(hq, hkv, nq, d, page, lens, prefix_len, seed=50, token_major=Tru
 
 @pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(map(str, c[:5])) + f"-{len(c[5])}-{c[6]}")
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
-def test_paged_decode(case, out_dtype):
+@pytest.mark.parametrize("keys", [0, 40000])  # what the table can hold: narrow tables take clusters
+def test_paged_decode(case, out_dtype, keys):
     hq, hkv, nq, d, page, lens, prefix_len = case
-    q, kp, vp, table, prefix = decode_case(*case, token_major=out_dtype is torch.float32)
+    q, kp, vp, table, prefix = decode_case(*case, token_major=out_dtype is torch.float32, width=keys // page)
     tol, tol_lse = P.tolerances(q, kp, vp, P_SPLIT, out_dtype)
     o_ref, l_ref = P.decode(q, kp, vp, table, lens, prefix, prefix_len)
     poison(kp, vp, table, lens, page, prefix, prefix_len)
@@ -196,7 +197,7 @@ def test_paged_decode_random(i):
     lens = [int(x) for x in r.integers(0, int(r.choice([20, 300, 2500])), int(r.integers(1, 12)))]
     prefix_len = int(r.integers(1, 1500)) if r.random() < 0.4 else 0
     q, kp, vp, table, prefix = decode_case(hkv * g, hkv, nq, d, page, lens, prefix_len, 90 + i,
-                                           bool(r.integers(0, 2)))
+                                           bool(r.integers(0, 2)), int(r.choice([1, 40000 // page])))
     scale = float(r.choice([0.05, 0.125, 0.3]))
     tol, tol_lse = P.tolerances(q, kp, vp, P_SPLIT, torch.float32, scale)
     o_ref, l_ref = P.decode(q, kp, vp, table, lens, prefix, prefix_len, scale)
