@@ -275,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncthreads();  // the barriers
   } else {
     find_run<kStep>(p, sh.sums, &sh.place, t0, t1);
-    if (t0 >= t1) return;
-    x = sh.place;
+    x = sh.place;  // (of no use to a block without steps)
   }
   const int n_steps = static_cast<int>(t1 - t0);
   const uint32_t smem0 = smem_addr(smem);
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   };
-  if (computes) begin_unit();
+  if (computes && n_steps > 0) begin_unit();
   // ldmatrix rows of this lane: for K, 8 keys x 16 bytes of d per matrix, keys
   // 8..15 in the upper two; for V (transposed), keys 8..15 in the odd ones.  A
   // 128-byte line's 16-byte pieces are permuted by its address bits 7..9.
@@ -630,6 +629,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
     }
     cluster_sync();  // no CTA leaves while its rows are read
+  } else {
+    // a prefix launch that this one overlaps with (nothing of it is read here)
+    // has ended before this one has: the merge waits for this one alone
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   }
 }
 
@@ -784,29 +787,41 @@ int launch_clusters(const PageMaps& maps, const PagedDecodeParams& p, int64_t d,
                    : launch_clusters<64, 4>(maps, p, dev, s);
 }
 
+// early: the launch before is the shared prefix's; this one may start while
+// that one drains.
 template <int D, int RT>
-int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t grid, int device,
-               cudaStream_t s) {
+int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t grid, bool early,
+               int device, cudaStream_t s) {
   auto kern = paged_decode_kernel<D, RT, 1>;
   constexpr int smem = kSmem<D>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, smem, device, done)) return LSX_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
   timing_begin(kKidPagedDecode, s);
-  kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(maps.k, maps.v, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, p);
   timing_end(kKidPagedDecode, s);
-  return cudaGetLastError() == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
+  return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
 }
 
-int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t d, int64_t grid, int dev,
-               cudaStream_t s) {
+int launch_run(const PageMaps& maps, const PagedDecodeParams& p, int64_t d, int64_t grid,
+               bool early, int dev, cudaStream_t s) {
   const int rt = p.R <= 16 ? 1 : (p.R <= 32 ? 2 : 4);
   if (d == 128)
-    return rt == 1   ? launch_run<128, 1>(maps, p, grid, dev, s)
-           : rt == 2 ? launch_run<128, 2>(maps, p, grid, dev, s)
-                     : launch_run<128, 4>(maps, p, grid, dev, s);
-  return rt == 1   ? launch_run<64, 1>(maps, p, grid, dev, s)
-         : rt == 2 ? launch_run<64, 2>(maps, p, grid, dev, s)
-                   : launch_run<64, 4>(maps, p, grid, dev, s);
+    return rt == 1   ? launch_run<128, 1>(maps, p, grid, early, dev, s)
+           : rt == 2 ? launch_run<128, 2>(maps, p, grid, early, dev, s)
+                     : launch_run<128, 4>(maps, p, grid, early, dev, s);
+  return rt == 1   ? launch_run<64, 1>(maps, p, grid, early, dev, s)
+         : rt == 2 ? launch_run<64, 2>(maps, p, grid, early, dev, s)
+                   : launch_run<64, 4>(maps, p, grid, early, dev, s);
 }
 
 }  // namespace
@@ -882,7 +897,7 @@ int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const ls
       p.lens = nullptr;
       p.fixed_len = prefix_len;
       p.direct = 0;
-      rc = launch_run(maps, p, q.D, grid, ctx.device, s);
+      rc = launch_run(maps, p, q.D, grid, false, ctx.device, s);
     } else {
       const PrefixPlan plan = prefix_plan(q.B, per, hkv, prefix_len, ctx.sm_count);
       float* part_l = reinterpret_cast<float*>(ws);
@@ -912,7 +927,7 @@ int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const ls
   p.lens = kv_lens;
   p.fixed_len = 0;
   p.direct = prefix_len > 0 ? 0 : 1;
-  const int rc = launch_run(maps, p, q.D, grid, ctx.device, s);
+  const int rc = launch_run(maps, p, q.D, grid, prefix_len > 0, ctx.device, s);
   if (rc != LSX_OK) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(q.B * q.H * q.N, 8)));

@@ -120,8 +120,8 @@ def _table(t, batch):
 
 
 def _outputs(q, out, lse, out_dtype):
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if out is None:  # in the order of q's dimensions in memory
+        out = torch.empty_like(q, dtype=out_dtype)
     if lse is None:
         lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
     return out, lse
