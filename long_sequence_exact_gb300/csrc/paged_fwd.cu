@@ -49,9 +49,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // base 2: P <= 256 under a stale maximum
 constexpr int kOkRing = 8;                 // >= stages + 2 (see the loader)
+constexpr int kItems = 4;                  // items handed to the other roles ahead
 constexpr int kMinPiece = 4;               // key tiles
 constexpr int kPiecesPerSm = 4;            // at most, over all units and kv heads
 constexpr int kPlanThreads = 512;
+
+// What a CTA works on: tokens [tok0, tok0 + ntok) of sequence b (rows of up to
+// two tiles) against key tiles [j0, j0 + size); the first token's last visible
+// key is lim0 (causal; each next token sees one more) and there are len keys.
+struct __align__(16) Entry {
+  int32_t b, tok0, ntok, j0, size, len, lim0, slot;  // slot < 0: the whole row range
+};
+struct Item {
+  Entry e;
+  int hk;    // < 0: no more items
+  int n[2];  // key tiles of query tile t
+  int pad;
+};
 
 template <int D>
 struct Cfg {
@@ -72,18 +86,14 @@ struct __align__(1024) Smem {
   uint64_t k_empty[Cfg<D>::kStages];
   uint64_t v_empty[Cfg<D>::kStages];
   uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  Item item[kItems];
   uint32_t keys_ok[kOkRing];  // bit g: keys [16 g, 16 g + 16) of the tile exist
   uint32_t tail_stage;
   uint32_t tmem_base;
   int abort;
 };
 
-// What a CTA works on: tokens [tok0, tok0 + ntok) of sequence b (rows of up to
-// two tiles) against key tiles [j0, j0 + size); the first token's last visible
-// key is lim0 (causal; each next token sees one more) and there are len keys.
-struct __align__(16) Entry {
-  int32_t b, tok0, ntok, j0, size, len, lim0, slot;  // slot < 0: the whole row range
-};
 // A cut unit for the merge: pieces first, .., first + n - 1.
 struct __align__(16) CutUnit {
   int32_t tok0, ntok, first, n;
@@ -105,12 +115,6 @@ struct FwdParams {
   float* part_l;  // [slot][Hkv][256]
   int* status;
   uint64_t wait_ns;
-};
-
-struct Item {
-  Entry e;
-  int hk;
-  int n[2];  // key tiles of query tile t
 };
 
 __device__ __forceinline__ int64_t item_count(const FwdParams& p) {
@@ -201,6 +205,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&sm.k_empty[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], 10);  // MMA thread, clearing warp, 8 softmax warps
+    }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.s_full[t], 1);
       mbar_init(&sm.p_full[t], 128);
@@ -240,9 +248,18 @@ __global__ void __launch_bounds__(384, 1)
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
       };
       for (int64_t r = 0;; ++r) {
+        // (decoded here, ahead of time, and handed to the other roles in a slot)
         const int64_t it = snake_item(c, r, grid);
-        if (it >= n_items) break;
-        const Item x = get_item(p, it, n_entries);
+        const int slot = static_cast<int>(r % kItems);
+        Item x;
+        if (it < n_items) x = get_item(p, it, n_entries);
+        else x.hk = -1;
+        if (r >= kItems && !wait_all(&sm.item_empty[slot], ((r / kItems) & 1) ^ 1)) break;
+        if (lane == 0) {
+          sm.item[slot] = x;
+          mbar_arrive(&sm.item_full[slot]);
+        }
+        if (x.hk < 0) break;
         const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
         // page of each 16-key group of a tile in lanes 0..7, a tile ahead
         const int32_t* row = p.c.table + x.e.b * p.c.table_stride;
@@ -315,12 +332,14 @@ __global__ void __launch_bounds__(384, 1)
                  kIdS, kk > 0 ? 1u : 0u);
         mma_commit(&sm.s_full[t]);
       };
-      for (int64_t r = 0;; ++r) {
-        const int64_t it = snake_item(c, r, grid);
-        if (it >= n_items) break;
-        const Item x = get_item(p, it, n_entries);
-        const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
+      for (uint32_t r = 0;; ++r) {
+        if (!mbar_wait(&sm.item_full[r % kItems], (r / kItems) & 1, guard)) break;
+        const Item& x = sm.item[r % kItems];
+        if (x.hk < 0) break;
+        const int n0 = x.n[0], n1 = x.n[1];
+        const int nkv = n0 > n1 ? n0 : n1;
         const int tail = tail_tile(p, x.e, nkv);
+        mbar_arrive(&sm.item_empty[r % kItems]);
         if (!mbar_wait(&sm.q_full, q_phase, guard)) break;
         q_phase ^= 1;
         tc_fence_after();
@@ -329,11 +348,13 @@ __global__ void __launch_bounds__(384, 1)
           if (!mbar_wait(&sm.k_full[kst], kph, guard)) break;
           tc_fence_after();
           for (int t = 0; t < 2; ++t)
-            if (x.n[t] > 0) issue_s(t, smem_addr(sm.k[kst]));
+            if ((t == 0 ? n0 : n1) > 0) issue_s(t, smem_addr(sm.k[kst]));
           issued = true;
           mma_commit(&sm.k_empty[kst]);
           if (++kst == kStages) { kst = 0; kph ^= 1; }
         }
+        // Q is free for the next item once the last S products are done
+        if (nkv <= 1) mma_commit(&sm.q_empty);
         for (int j = 0; j < nkv; ++j) {
           if (!mbar_wait(&sm.v_full[vst], vph, guard)) { ok = false; break; }
           if (j == tail) {
@@ -347,7 +368,8 @@ __global__ void __launch_bounds__(384, 1)
           const bool has_next = j + 1 < nkv;
           bool k_ready = false;
           for (int t = 0; t < 2; ++t) {
-            if (j < x.n[t]) {
+            const int nt = t == 0 ? n0 : n1;
+            if (j < nt) {
               if (!mbar_wait(&sm.p_full[t], p_phase[t], guard)) { ok = false; break; }
               p_phase[t] ^= 1;
               tc_fence_after();
@@ -358,7 +380,7 @@ __global__ void __launch_bounds__(384, 1)
                        kk > 0 ? 1u : acc0);
               mma_commit(&sm.o_full[t]);
             }
-            if (has_next && j + 1 < x.n[t]) {
+            if (has_next && j + 1 < nt) {
               if (!k_ready) {
                 if (!mbar_wait(&sm.k_full[kst], kph, guard)) { ok = false; break; }
                 tc_fence_after();
@@ -374,12 +396,12 @@ __global__ void __launch_bounds__(384, 1)
             }
             mma_commit(&sm.k_empty[kst]);
             if (++kst == kStages) { kst = 0; kph ^= 1; }
+            if (j + 2 == nkv) mma_commit(&sm.q_empty);
           }
           mma_commit(&sm.v_empty[vst]);
           if (++vst == kStages) { vst = 0; vph ^= 1; }
         }
         if (!ok) break;
-        mma_commit(&sm.q_empty);
       }
       if (issued) {  // every product has completed before TMEM is released
         mma_commit(&sm.final_bar);
@@ -389,12 +411,15 @@ __global__ void __launch_bounds__(384, 1)
       // --------------------------------- value rows past the last key
       // (when the MMA thread asks for it: it knows the stage, and waits)
       uint32_t phase = 0;
-      for (int64_t r = 0;; ++r) {
-        const int64_t it = snake_item(c, r, grid);
-        if (it >= n_items) break;
-        const Item x = get_item(p, it, n_entries);
+      for (uint32_t r = 0;; ++r) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(&sm.item_full[r % kItems], (r / kItems) & 1, guard);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        const Item x = sm.item[r % kItems];
+        if (x.hk < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[r % kItems]);
         if (tail_tile(p, x.e, x.n[0] > x.n[1] ? x.n[0] : x.n[1]) >= 0) {
-          int ok = 1;
           if (lane == 0) ok = mbar_wait(&sm.v_tail, phase, guard);
           if (!__shfl_sync(0xffffffffu, ok, 0)) break;
           phase ^= 1;
@@ -426,12 +451,12 @@ __global__ void __launch_bounds__(384, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return mbar_wait(bar, parity, WaitGuard{p.status, p.wait_ns, &sm.abort});
     };
-    for (int r = 0;; ++r) {
-      const int64_t it = snake_item(blockIdx.x, r, gridDim.x);
-      if (it >= n_items) break;
+    for (uint32_t r = 0;; ++r) {
+      if (!wait(&sm.item_full[r % kItems], (r / kItems) & 1)) break;
       int nkv, kb, lim, lim_tile, tiles;
       {
-        const Item x = get_item(p, it, n_entries);
+        const Item& x = sm.item[r % kItems];
+        if (x.hk < 0) break;
         nkv = x.n[t];
         tiles = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
         kb = x.e.j0 * 128;
@@ -537,7 +562,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       count += tiles;
       // ------------------------------------------------------- epilogue
-      const Item x = get_item(p, it, n_entries);
+      const Item& x = sm.item[r % kItems];
       const int tok = row / p.per, rem = row - tok * p.per;
       const bool valid = tok < tile_tokens(p, x.e, t);
       if (nkv > 0) {
@@ -589,6 +614,8 @@ __global__ void __launch_bounds__(384, 1)
         else
           static_cast<float*>(p.lse.data)[view_off(p.lse, 0, h, token)] = lse;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[r % kItems]);
     }
   }
 
@@ -645,6 +672,7 @@ constexpr int kBuckets = 64;
 // list of work, longest pieces first.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int32_t start[];  // [batch + 1] first pair of each sequence
+  Seq* const seqs = reinterpret_cast<Seq*>(start + p.batch + 1);
   __shared__ int32_t wsum[kPlanThreads / 32];
   __shared__ int32_t tiles[kCutUnits], slot0[kCutUnits];
   __shared__ int32_t hist[kBuckets + 1];
@@ -662,6 +690,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   int32_t mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = plan_seq(p, b);
+    seqs[b] = s;
     start[b] = mine;
     mine += (s.n + pair_tok - 1) / pair_tok;
     if (s.len > p.cap && s.n > 0) atomicCAS(p.status, 0, kStatusPage);
@@ -689,7 +718,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
       const int mid = (lo + hi) >> 1;
       if (start[mid] <= i) lo = mid; else hi = mid;
     }
-    s = plan_seq(p, lo);
+    s = seqs[lo];
     first = (i - start[lo]) * pair_tok;
     return lo;
   };
@@ -705,7 +734,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     if (may_cut) tiles[i] = n;
     top = n > top ? n : top;
   }
-  if (top > 0) atomicMax(&longest, top);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0 && top > 0) atomicMax(&longest, top);
   __syncthreads();
   int32_t piece = longest > 0 ? longest : 1;
   if (may_cut && longest >= 2 * kMinPiece) {
@@ -714,6 +744,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     // partials), and the merge (54 pieces of 128 KB a tile's time, 3 to start)
     const int k = t + 1;
     const int32_t w = (longest + k - 1) / k;
+    unsigned long long mine_best = ~0ull;
     if (k == 1 || w >= kMinPiece) {
       int64_t n = 0;
       for (int i = 0; i < n_pairs; ++i) n += tiles[i] > w ? (tiles[i] + w - 1) / w : 1;
@@ -721,10 +752,15 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
         const int64_t all = n * p.Hkv, rounds = (all + p.sm_count - 1) / p.sm_count;
         // (as cut_cost; an uncut unit writes its result itself)
         const float cost = rounds * (w + (k > 1 ? 1.5f : 0.f)) + (k > 1 ? 3.f + all / 54.f : 0.f);
-        atomicMin(&best, (static_cast<unsigned long long>(cost * 16.f) << 32) |
-                             static_cast<unsigned>(w));
+        mine_best = (static_cast<unsigned long long>(cost * 16.f) << 32) | static_cast<unsigned>(w);
       }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const unsigned long long o = __shfl_xor_sync(0xffffffffu, mine_best, d);
+      mine_best = o < mine_best ? o : mine_best;
+    }
+    if (lane == 0 && mine_best != ~0ull) atomicMin(&best, mine_best);
     __syncthreads();
     piece = static_cast<int32_t>(best & 0xffffffffu);
   }
@@ -769,18 +805,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   };
   const int rounds = longest > piece ? (longest + piece - 1) / piece : 1;  // a unit's most pieces
   auto each = [&](auto&& f) {  // piece-major
-    for (int j = 0; j < rounds; ++j)
-      for (int i = t; i < n_pairs; i += kPlanThreads) {
-        Seq s;
-        int32_t first, size;
-        const int b = unit(i, s, first);
-        const int32_t nt = s.n - first < pair_tok ? s.n - first : pair_tok;
-        const int32_t n = pair_tiles(p.cap, s, first + nt - 1);
-        const int32_t k = cut(n, size);
-        if (j >= k) continue;
-        const int32_t left = n - j * size;
-        f(i, j, k, b, s, first, nt, left < size ? left : size, size);
-      }
+    for (int64_t at = t; at < static_cast<int64_t>(rounds) * n_pairs; at += kPlanThreads) {
+      const int j = static_cast<int>(at / n_pairs), i = static_cast<int>(at % n_pairs);
+      Seq s;
+      int32_t first, size;
+      const int b = unit(i, s, first);
+      const int32_t nt = s.n - first < pair_tok ? s.n - first : pair_tok;
+      const int32_t n = pair_tiles(p.cap, s, first + nt - 1);
+      const int32_t k = cut(n, size);
+      if (j >= k) continue;
+      const int32_t left = n - j * size;
+      f(i, j, k, b, s, first, nt, left < size ? left : size, size);
+    }
   };
   each([&](int, int, int, int, const Seq&, int32_t, int32_t, int32_t now, int32_t) {
     atomicAdd(&hist[bucket(now) + 1], 1);
@@ -823,7 +859,7 @@ struct FwdMergeParams {
 
 // One warp per row of a cut unit.
 template <int D>
-__global__ void __launch_bounds__(256) paged_fwd_merge_kernel(const FwdMergeParams p) {
+__global__ void __launch_bounds__(256, 3) paged_fwd_merge_kernel(const FwdMergeParams p) {
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t rows = __ldcg(&p.header->n_cut) * p.Hkv * 256;
@@ -1026,7 +1062,12 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   pp.cut = reinterpret_cast<CutUnit*>(ws + x.cut);
   pp.status = ctx.status;
   timing_begin(kKidPagedPlan, s);
-  paged_plan_kernel<<<1, kPlanThreads, (batch + 1) * sizeof(int32_t), s>>>(pp);
+  const int plan_smem = static_cast<int>((batch + 1) * sizeof(int32_t) + batch * sizeof(Seq));
+  static std::atomic<uint64_t> done{0};
+  if (plan_smem > 40 * 1024 &&
+      !allow_smem(paged_plan_kernel, kMaxMapBatch * 16 + 16, ctx.device, done))
+    return LSX_ERR_LAUNCH;
+  paged_plan_kernel<<<1, kPlanThreads, plan_smem, s>>>(pp);
   timing_end(kKidPagedPlan, s);
   if (cudaGetLastError() != cudaSuccess) return LSX_ERR_LAUNCH;
   const int64_t most = x.max_entries * p.Hkv;
