@@ -96,9 +96,7 @@ __device__ __forceinline__ int32_t unit_steps(int32_t len) {
 
 // A place in the run: unit (b, hk), its length and steps, the step.
 struct Cursor {
-  int64_t b;
-  int hk;
-  int32_t len, steps, step;
+  int32_t b, hk, len, steps, step;
 };
 template <int kStep>
 __device__ __forceinline__ void advance(const PagedDecodeParams& p, Cursor& x) {
@@ -112,15 +110,35 @@ __device__ __forceinline__ void advance(const PagedDecodeParams& p, Cursor& x) {
   }
 }
 
-// Sums the steps of all units and finds this block's run of them, steps
-// [t0, t1), and the unit that holds t0; block 0 writes the starts.
+// Where the runs are cut.  A unit costs its steps and `extra` more (its queries'
+// loads, the join of the warps, the result: about two steps' time), so that a
+// run of many short units is no longer than one of a few long ones; nothing
+// extra where the runs are a few steps, which then spread best one by one.  With
+// u units (sequences) of n_u steps, unit (b, hk) begins at place
+// (S_b + extra b) Hkv + hk (n_b + extra) of a line of (S + extra u) Hkv places, its
+// step i at `extra` + i behind that; run c of g is [c all / g, (c + 1) all / g).
+constexpr int64_t kUnitExtra = 2;
+__device__ __forceinline__ int64_t unit_extra(int64_t steps, int64_t hkv, int64_t grid) {
+  return steps * hkv >= 4 * grid ? kUnitExtra : 0;
+}
+__device__ __forceinline__ int64_t run_count(int64_t all, int64_t grid) {
+  return all < grid ? all : grid;
+}
+
+struct Run {
+  Cursor from;     // the first step
+  int64_t s0, s1;  // steps of the whole line before the run, and at its end
+};
+
+// Sums the steps of all units and finds this block's run; block 0 writes the
+// sums for the merge.
 template <int kStep>
-__device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* sums, Cursor* place,
-                                         int64_t& t0, int64_t& t1) {
+__device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* sums, Run* run) {
   const int t = threadIdx.x;
-  const int64_t per = (p.units_b + kThreads - 1) / kThreads;
-  const int64_t b0 = t * per < p.units_b ? t * per : p.units_b;
-  const int64_t b1 = b0 + per < p.units_b ? b0 + per : p.units_b;
+  const int64_t h = p.rows.Hkv, units = p.units_b;
+  const int64_t per = (units + kThreads - 1) / kThreads;
+  const int64_t b0 = t * per < units ? t * per : units;
+  const int64_t b1 = b0 + per < units ? b0 + per : units;
   int64_t mine = 0;
   for (int64_t b = b0; b < b1; ++b) mine += unit_steps<kStep>(unit_len(p, b));
   int64_t inc = mine;
@@ -137,31 +155,43 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
     if (w < (t >> 5)) before += sums[w];
     total += sums[w];
   }
-  const int64_t all = total * p.rows.Hkv;
-  const int64_t g = all < gridDim.x ? all : gridDim.x;  // runs: none is empty
-  t0 = blockIdx.x < g ? blockIdx.x * all / g : all;
-  t1 = blockIdx.x < g ? (blockIdx.x + 1) * all / g : all;
-  // the thread whose sequences hold step t0 finds the unit
-  const int64_t h = p.rows.Hkv;
-  if (t0 >= before * h && t0 < (before + mine) * h) {
-    int64_t at = before;
+  const int64_t extra = unit_extra(total, h, gridDim.x);
+  const int64_t all = (total + extra * units) * h, g = run_count(all, gridDim.x);
+  const int64_t c = blockIdx.x;
+#pragma unroll
+  for (int end = 0; end < 2; ++end) {
+    const int64_t at = c < g ? (c + end) * all / g : all;
+    int64_t* out = end == 0 ? &run->s0 : &run->s1;
+    if (at == all) {
+      if (t == 0) *out = total * h;
+      continue;
+    }
+    // the thread whose sequences hold this place finds the unit
+    if (at < (before + extra * b0) * h || at >= (before + mine + extra * b1) * h) continue;
+    int64_t steps = before;
     for (int64_t b = b0; b < b1; ++b) {
       const int32_t len = unit_len(p, b), n = unit_steps<kStep>(len);
-      if (t0 < (at + n) * h) {
-        const int64_t r = t0 - at * h;
-        *place = Cursor{b, static_cast<int>(r / n), len, n, static_cast<int32_t>(r % n)};
+      if (at < (steps + n + extra * (b + 1)) * h) {
+        const int64_t r = at - (steps + extra * b) * h;
+        const int64_t hk = r / (n + extra);
+        int64_t step = r - hk * (n + extra) - extra;
+        if (step < 0) step = 0;
+        *out = steps * h + hk * n + step;
+        if (end == 0)
+          run->from = Cursor{static_cast<int32_t>(b), static_cast<int32_t>(hk), len, n,
+                             static_cast<int32_t>(step)};
         break;
       }
-      at += n;
+      steps += n;
     }
   }
   if (blockIdx.x == 0) {
-    int64_t at = before;
+    int64_t steps = before;
     for (int64_t b = b0; b < b1; ++b) {
-      p.start[b] = at;
-      at += unit_steps<kStep>(unit_len(p, b));
+      p.start[b] = steps;
+      steps += unit_steps<kStep>(unit_len(p, b));
     }
-    if (t == kThreads - 1) p.start[p.units_b] = total;
+    if (t == 0) p.start[units] = total;
     if (p.lens != nullptr) {
       const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.shift;
       for (int64_t b = b0; b < b1; ++b)
@@ -174,7 +204,7 @@ __device__ __forceinline__ void find_run(const PagedDecodeParams& p, int64_t* su
 // What a CTA keeps in shared memory behind the stages and the join's buffer.
 struct Shared {
   int64_t sums[kThreads / 32];
-  Cursor place;
+  Run run;
   uint64_t full[3], empty[3];
   uint32_t pages_ok[3];     // bit i: 16-key group i of the stage exists
   int abort;
@@ -217,12 +247,13 @@ __device__ __forceinline__ void compute_sync() {
 }
 
 // Output row of unit row r, false when there is none.
-__device__ __forceinline__ bool out_row(const PagedDecodeParams& p, int64_t ub, int hk, int r,
+__device__ __forceinline__ bool out_row(const PagedDecodeParams& p, int ub, int hk, int r,
                                         int64_t& b, int64_t& h, int64_t& n) {
-  const int64_t gr = ub * p.R + r;
-  b = gr / p.rows.per;
-  if (r >= p.R || b >= p.rows.B) return false;
-  const int rem = static_cast<int>(gr - b * p.rows.per), g = rem / p.rows.Nq;
+  const int gr = ub * p.R + r;  // (fewer than 2^16 sequences of 64 rows)
+  const int bb = gr / p.rows.per;
+  if (r >= p.R || bb >= p.rows.B) return false;
+  const int rem = gr - bb * p.rows.per, g = rem / p.rows.Nq;
+  b = bb;
   n = rem - g * p.rows.Nq;
   h = static_cast<int64_t>(hk) * p.rows.G + g;
   return true;
@@ -257,27 +288,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
   }
-  int64_t t0, t1;
+  int n_steps;
   const uint32_t rank = CL > 1 ? cluster_rank() : 0;
   Cursor x;
   if constexpr (CL > 1) {
-    const int64_t unit = blockIdx.x / CL;
-    x.b = unit / p.rows.Hkv;
-    x.hk = static_cast<int>(unit - x.b * p.rows.Hkv);
+    const int32_t unit = blockIdx.x / CL, hkv = static_cast<int32_t>(p.rows.Hkv);
+    x.b = unit / hkv;
+    x.hk = unit - x.b * hkv;
     x.len = unit_len(p, x.b);
     x.steps = unit_steps<kStep>(x.len);
-    t0 = static_cast<int64_t>(x.steps) * rank / CL;
-    t1 = static_cast<int64_t>(x.steps) * (rank + 1) / CL;
-    x.step = static_cast<int32_t>(t0);
+    x.step = static_cast<int32_t>(static_cast<int64_t>(x.steps) * rank / CL);
+    n_steps = static_cast<int32_t>(static_cast<int64_t>(x.steps) * (rank + 1) / CL) - x.step;
     if (threadIdx.x == 0 && rank == 0 &&
         __ldg(p.lens + x.b) > static_cast<int64_t>(p.c.max_pages) << p.c.shift)
       atomicCAS(p.status, 0, kStatusPage);
     __syncthreads();  // the barriers
   } else {
-    find_run<kStep>(p, sh.sums, &sh.place, t0, t1);
-    x = sh.place;  // (of no use to a block without steps)
+    find_run<kStep>(p, sh.sums, &sh.run);
+    x = sh.run.from;  // (of no use to a block without steps)
+    n_steps = static_cast<int>(sh.run.s1 - sh.run.s0);
   }
-  const int n_steps = static_cast<int>(t1 - t0);
   const uint32_t smem0 = smem_addr(smem);
 
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column
@@ -307,6 +337,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         atomicCAS(p.status, 0, kStatusPage);
       advance<kStep>(p, ld);
       next = fetch(n_steps - it - 1);
+      if (ld.step == 0 && it + 1 < n_steps) {  // the next unit's queries
+        for (int r = lane; r < p.R; r += 32) {
+          int64_t b, h, n;
+          if (out_row(p, ld.b, ld.hk, r, b, h, n)) {
+            const __nv_bfloat16* q = p.q + b * p.q_sb + h * p.q_sh + n * p.q_sn;
+#pragma unroll
+            for (int i = 0; i < D; i += 64)
+              asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+          }
+        }
+      }
       const uint32_t mask = __ballot_sync(0xffffffffu, exists);
       const int page = __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * per) & 31);
       const int stage = it % kS;
@@ -528,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // a cut unit: the run's first slot when it began in an earlier run, its
         // second when it goes on in a later one
         const int64_t slot = whole && unit_end
-                                 ? p.whole_slot0 + x.b * p.rows.Hkv + x.hk
+                                 ? p.whole_slot0 + static_cast<int64_t>(x.b) * p.rows.Hkv + x.hk
                                  : 2 * static_cast<int64_t>(blockIdx.x) + (whole ? 1 : 0);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -643,18 +684,16 @@ struct RunView {
   int R;
   PartView part;
 };
-// Slots of unit (b, hk): those of runs first..last, run c at slot 2 c, or
-// 2 c + 1 where the unit begins in it; a unit in one run has its own.
+// Slots of unit (b, hk): those of runs first..last; the unit begins in the first,
+// slot 2 first + 1, and goes on in the others, slot 2 c.  A unit in one run has its own.
 __device__ __forceinline__ void unit_runs(const RunView& v, int64_t b, int64_t hk, int64_t& first,
-                                          int64_t& last, bool& begins) {
-  const int64_t s0 = __ldcg(v.start + b), s1 = __ldcg(v.start + b + 1);
-  const int64_t all = __ldcg(v.start + v.units) * v.hkv;
-  const int64_t a = s0 * v.hkv + hk * (s1 - s0), z = a + (s1 - s0) - 1;
-  // run c covers steps [c all / g, (c + 1) all / g)
-  const int64_t g = all < v.grid ? all : v.grid;
+                                          int64_t& last) {
+  const int64_t s0 = __ldcg(v.start + b), n = __ldcg(v.start + b + 1) - s0;
+  const int64_t total = __ldcg(v.start + v.units), extra = unit_extra(total, v.hkv, v.grid);
+  const int64_t all = (total + extra * v.units) * v.hkv, g = run_count(all, v.grid);
+  const int64_t a = (s0 + extra * b) * v.hkv + hk * (n + extra) + extra, z = a + n - 1;
   first = ((a + 1) * g - 1) / all;
   last = ((z + 1) * g - 1) / all;
-  begins = a >= first * all / g;
 }
 
 // The prompt kernel's partials of a shared prefix (pieces 0: none).
@@ -686,12 +725,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams
   RowMerge<D> sum;
   auto take = [&](const RunView& v) {
     int64_t first, last;
-    bool begins;
     const int64_t u = gr / v.R, r = gr - u * v.R;
-    unit_runs(v, u, hk, first, last, begins);
+    unit_runs(v, u, hk, first, last);
     sum.take(v.part.o, v.part.l, last - first + 1, lane, [&](int64_t i) {
       const int64_t slot = first == last ? v.whole_slot0 + u * v.hkv + hk
-                                         : 2 * (first + i) + (i == 0 && begins ? 1 : 0);
+                                         : 2 * (first + i) + (i == 0 ? 1 : 0);
       return slot * v.R + r;
     });
   };
@@ -706,8 +744,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedMergeParams
     take(p.prefix);
   } else {
     int64_t first, last;
-    bool begins;
-    unit_runs(p.own, b, hk, first, last, begins);
+    unit_runs(p.own, b, hk, first, last);
     if (first == last) return;
   }
   take(p.own);
