@@ -446,12 +446,14 @@ __global__ void __launch_bounds__(384, 1)
         }
         float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
-        for (int i = 4; i < 128; i += 8) {
+        for (int i = 4; i < 124; i += 8) {
           mx0 = fmax3(mx0, s[i], s[i + 1]);
           mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
           mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
           mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
         }
+        mx0 = fmax3(mx0, s[124], s[125]);
+        mx1 = fmax3(mx1, s[126], s[127]);
         const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
         const float m_new = fmaxf(m, mx * sl2);
         if (j == 0) {
