@@ -348,7 +348,7 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *     [P, page, Hkv, D] storage is the same view with other strides.
  *   block_table: device int32 [batch][max_pages], rows table_stride entries
  *     apart; position i of sequence b is row i % page of page
- *     block_table[b][i / page].  max_pages * page < 2^31.
+ *     block_table[b][i / page].  max_pages * page <= 2^31 - 512.
  *   kv_lens: device int32 [batch], the keys of each sequence, the new tokens'
  *     own keys among them.
  * Lengths, tables and slots are read on the device when the call runs, so a
@@ -391,7 +391,7 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *
  * attn_paged_fwd -- prompts: ragged query tokens, causal, over the cache.
  *   q [1, Hq, T, D] bf16, the tokens of sequence b at [cu_q[b], cu_q[b + 1])
- *   (device int32 [batch + 1], ascending, batch <= 4096); the i-th of its n
+ *   (device int32 [batch + 1], ascending, batch <= 4096; cut to [0, T]); the i-th of its n
  *   tokens sees keys j <= kv_len - n + i.  Hq / Hkv <= 128.  o, lse as q; rows
  *   that belong to no sequence are left as they were.  P is rounded to bf16.
  *

@@ -47,8 +47,8 @@ int check_ints(const void* p) {
 // block table [batch][max_pages], rows table_stride apart
 int check_table(const int32_t* table, int64_t table_stride, int64_t max_pages, int64_t page) {
   if (max_pages < 0 || table_stride < max_pages) return LSX_ERR_SHAPE;
-  // positions are 32-bit
-  if (max_pages * page >= (int64_t{1} << 31) || max_pages >= (int64_t{1} << 31))
+  // positions, rounded up to a tile, are 32-bit
+  if (max_pages >= (int64_t{1} << 31) || max_pages * page > (int64_t{1} << 31) - 2 * kMaxPage)
     return LSX_ERR_UNSUPPORTED;
   return max_pages == 0 ? LSX_OK : check_ints(table);
 }
@@ -138,7 +138,7 @@ int attn_paged_decode(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_
   LSX_TRY(check_table(block_table, table_stride, max_pages, k_pages->N));
   LSX_TRY(check_ints(kv_lens));
   if (prefix_len < 0) return LSX_ERR_SHAPE;
-  if (prefix_len >= (int64_t{1} << 31) - kMaxPage) return LSX_ERR_UNSUPPORTED;
+  if (prefix_len > (int64_t{1} << 31) - 2 * kMaxPage) return LSX_ERR_UNSUPPORTED;
   if (prefix_len > 0) LSX_TRY(check_ints(prefix_table));
   LSX_TRY(check_ws(workspace, workspace_bytes,
                    attn_paged_decode_workspace_size(q, k_pages, max_pages, prefix_len)));

@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(384, 1)
     regs_dec<104>();
     if (warp == 0) {
       // ---------------------------------------------------------- loader
-      uint32_t stage = 0, phase = 0, qe_phase = 0, count = 0;
+      uint32_t stage = 0, phase = 0, qe_phase = 0;
+      uint32_t count = 0, k_count = 0;  // key tiles loaded; their keys
       const int boxes = p.c.shift >= 7 ? 1 : 128 >> p.c.shift;  // per 64-column half
       const int rows = 128 / boxes;
       const int box = lane % boxes, sub = lane / boxes;
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(384, 1)
           if (lane < boxes * C::kSub)
             tma_load_4d(&sm.k[stage][sub * 128 * 64 + box * rows * 64], &tm_k, &sm.k_full[stage],
                         sub * 64, prow, x.hk, page);
+          k_count = count + 1;
           if (!wait_all(&sm.v_empty[stage], phase ^ 1)) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[stage], C::kTileBytes);
           __syncwarp();
@@ -312,6 +314,14 @@ __global__ void __launch_bounds__(384, 1)
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
+      }
+      if (lane == 0 && *guard.abort != 0) {
+        // gave up: the copies in flight land before the block ends
+        drain_wait(&sm.q_full, qe_phase ^ 1, p.wait_ns);
+        for (uint32_t i = count > kStages ? count - kStages : 0; i < k_count; ++i) {
+          drain_wait(&sm.k_full[i % kStages], (i / kStages) & 1, p.wait_ns);
+          if (i < count) drain_wait(&sm.v_full[i % kStages], (i / kStages) & 1, p.wait_ns);
+        }
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------ MMA issuer
@@ -673,7 +683,7 @@ constexpr int kBuckets = 64;
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int32_t start[];  // [batch + 1] first pair of each sequence
   Seq* const seqs = reinterpret_cast<Seq*>(start + p.batch + 1);
-  __shared__ int32_t wsum[kPlanThreads / 32];
+  __shared__ int64_t wsum[kPlanThreads / 32];
   __shared__ int32_t tiles[kCutUnits], slot0[kCutUnits];
   __shared__ int32_t hist[kBuckets + 1];
   __shared__ unsigned long long best;
@@ -687,31 +697,34 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
   const int b0 = t * per < p.batch ? t * per : p.batch;
   const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
-  int32_t mine = 0;
+  int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = plan_seq(p, b);
     seqs[b] = s;
-    start[b] = mine;
     mine += (s.n + pair_tok - 1) / pair_tok;
     if (s.len > p.cap && s.n > 0) atomicCAS(p.status, 0, kStatusPage);
   }
-  int32_t inc = mine;
+  int64_t inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += o;
   }
   if (lane == 31) wsum[t >> 5] = inc;
   __syncthreads();
-  int32_t before = inc - mine, n_pairs = 0;
+  int64_t before = inc - mine, all_pairs = 0;
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < (t >> 5)) before += wsum[w];
-    n_pairs += wsum[w];
+    all_pairs += wsum[w];
   }
-  for (int b = b0; b < b1; ++b) start[b] += before;
+  // (more pairs than the workspace has room for: only if cu_q does not ascend)
+  const int32_t n_pairs = static_cast<int32_t>(all_pairs < p.max_entries ? all_pairs : p.max_entries);
+  for (int b = b0; b < b1; ++b) {
+    start[b] = static_cast<int32_t>(before < n_pairs ? before : n_pairs);
+    before += (seqs[b].n + pair_tok - 1) / pair_tok;
+  }
   if (t == 0) start[p.batch] = n_pairs;
   __syncthreads();
-  if (n_pairs > p.max_entries) n_pairs = p.max_entries;  // (cu_q not ascending)
   auto unit = [&](int i, Seq& s, int32_t& first) -> int32_t {
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {

@@ -28,7 +28,17 @@ struct MapParams {
   int32_t* taken;
 };
 
-__device__ __forceinline__ int32_t clamp0(int32_t x) { return x < 0 ? 0 : x; }
+// A sequence's keys before and after the step: negative counts as none, and the
+// sum stays where rounding it up to a page does not overflow.
+constexpr int32_t kMostKeys = 0x7ffffe00;
+__device__ __forceinline__ int32_t keys_before(const MapParams& p, int b) {
+  const int32_t c = p.ctx[b];
+  return c < 0 ? 0 : (c > kMostKeys ? kMostKeys : c);
+}
+__device__ __forceinline__ int32_t keys_added(const MapParams& p, int b, int32_t before) {
+  const int32_t n = p.add[b];
+  return n < 0 ? 0 : (n > kMostKeys - before ? kMostKeys - before : n);
+}
 
 // Last index i with start[i] <= x (start ascending, start[0] = 0).
 __device__ __forceinline__ int find_seq(const int32_t* start, int n, int32_t x) {
@@ -59,7 +69,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
   int32_t sum_new = 0, sum_take = 0;
   for (int b = b0; b < b1; ++b) {
-    const int32_t c = clamp0(p.ctx[b]), n = clamp0(p.add[b]);
+    const int32_t c = keys_before(p, b), n = keys_added(p, b, c);
     cu[b] = sum_new;
     off[b] = sum_take;
     sum_new += n;
@@ -99,29 +109,33 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
   const int64_t step = static_cast<int64_t>(gridDim.x) * kMapThreads;
   for (int64_t b = first; b <= p.batch; b += step) {
     p.cu[b] = cu[b];
-    if (b < p.batch)
-      p.kv_lens[b] = clamp0(p.ctx[b]) + clamp0(p.add[b]);
-    else
+    if (b < p.batch) {
+      const int32_t c = keys_before(p, static_cast<int>(b));
+      p.kv_lens[b] = c + keys_added(p, static_cast<int>(b), c);
+    } else {
       *p.taken = pages;
+    }
   }
+  // (sums that pass 31 bits wrap: what they give is wrong then, but every place
+  // that is read or written is checked)
   for (int64_t i = first; i < pages; i += step) {
     const int b = find_seq(off, p.batch, static_cast<int32_t>(i));
-    const int64_t col = ((clamp0(p.ctx[b]) + mask) >> p.shift) + (i - off[b]);
+    const int64_t col = ((keys_before(p, b) + mask) >> p.shift) + (i - off[b]);
     if (col < p.max_pages) p.table[b * p.table_stride + col] = i < p.n_free ? p.free_pages[i] : -1;
   }
   for (int64_t i = first; i < p.n_tokens; i += step) {
     int64_t slot = -1;
     if (i < total) {
       const int b = find_seq(cu, p.batch, static_cast<int32_t>(i));
-      const int32_t c = clamp0(p.ctx[b]);
-      const int32_t pos = c + (static_cast<int32_t>(i) - cu[b]);
-      const int32_t col = pos >> p.shift, have = (c + mask) >> p.shift;
+      const int32_t c = keys_before(p, b);
+      const int64_t j = i - cu[b];
+      const int64_t pos = c + j, col = pos >> p.shift, have = (c + mask) >> p.shift;
       int32_t page = -1;
-      if (col < p.max_pages) {
-        const int64_t at = static_cast<int64_t>(off[b]) + (col - have);
+      if (j < keys_added(p, b, c) && col < p.max_pages) {
+        const int64_t at = off[b] + (col - have);
         if (col < have)
           page = p.table[b * p.table_stride + col];
-        else if (at < p.n_free)
+        else if (at >= 0 && at < p.n_free)
           page = p.free_pages[at];
       }
       if (page >= 0) slot = (static_cast<int64_t>(page) << p.shift) + (pos & mask);
@@ -129,6 +143,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapParams p
     p.slots[i] = slot;
   }
 }
+
+constexpr int kAppendCtas = 32;  // per SM, at most
 
 struct AppendParams {
   const void* k;
@@ -158,16 +174,20 @@ __device__ __forceinline__ uint4 load8(const void* base, int64_t off) {
 // One thread per eight elements of a token's row (a 16-byte store), the
 // elements of a token next to each other: with rows and pages that keep a
 // token's heads together, a token is one contiguous stretch on both sides.
-template <bool kF32>
+// Bound: HBM.  32-bit indexes where they fit (a 64-bit division a piece costs
+// 8%); 40,001 fp32 rows of 8 heads x 64: 39.2 us at 8 CTAs an SM and 64-bit
+// indexes, 36.0 us, 6.6 TB/s, as it is; two or four pieces of a thread in flight
+// together are no faster.
+template <bool kF32, typename Index>
 __global__ void __launch_bounds__(256) page_append_kernel(const AppendParams p) {
-  const int per = p.heads * p.d8;
-  const int64_t n = p.n_tokens * per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    const int64_t tok = i / per;
+  const Index per = static_cast<Index>(p.heads * p.d8);
+  const Index n = static_cast<Index>(p.n_tokens) * per;
+  const Index step = static_cast<Index>(gridDim.x) * 256;
+  for (Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
+    const Index tok = i / per;
     const int r = static_cast<int>(i - tok * per);
     const int h = r / p.d8, e = (r - h * p.d8) * 8;
-    const int64_t slot = p.slots[tok];
+    const int64_t slot = __ldg(p.slots + tok);
     if (slot < 0) continue;
     if (slot >= p.n_slots) {
       atomicCAS(p.status, 0, kStatusPage);
@@ -224,13 +244,17 @@ int launch_page_append(const lsx_tensor& k, const lsx_tensor& v, const int64_t* 
   p.d8 = static_cast<int>(k.D / 8);
   p.shift = log2_of(k_pages.N);
   p.status = ctx.status;
-  int64_t grid = ceil_div(k.N * k.H * p.d8, 256);
-  if (grid > 8 * ctx.sm_count) grid = 8 * ctx.sm_count;
+  const int64_t pieces = k.N * k.H * p.d8;
+  int64_t grid = ceil_div(pieces, 256);
+  const int64_t most = kAppendCtas * static_cast<int64_t>(ctx.sm_count);
+  if (grid > most) grid = most;
+  const bool small = pieces < (int64_t{1} << 31);  // (unsigned: a grid more fits too)
   timing_begin(kKidPageAppend, s);
-  if (k.dtype == LSX_F32)
-    page_append_kernel<true><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
-  else
-    page_append_kernel<false><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+  auto kern = k.dtype == LSX_F32
+                  ? (small ? page_append_kernel<true, uint32_t> : page_append_kernel<true, int64_t>)
+                  : (small ? page_append_kernel<false, uint32_t>
+                           : page_append_kernel<false, int64_t>);
+  kern<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
   timing_end(kKidPageAppend, s);
   return cudaGetLastError() == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
 }

@@ -92,6 +92,22 @@ def test_page_map(batch, page, ctx_max, new_max, short):
         assert taken.cpu().tolist() == [ref[4]]
 
 
+@pytest.mark.parametrize("ctx,new", [
+    ([2 ** 31 - 1, 5, -2 ** 31], [1, 2 ** 31 - 1, 2 ** 31 - 1]), ([2 ** 31 - 1] * 3, [2 ** 31 - 1] * 3),
+    ([0] * 5, [2 ** 31 - 1] * 5),
+])
+def test_page_map_with_sums_past_31_bits_stays_inside_its_arrays(ctx, new):
+    """What such lengths give is not defined; nothing outside the outputs changes."""
+    b = len(ctx)
+    whole = torch.full((b + 2, 9), 77, dtype=torch.int32, device=DEV)
+    free = ints([3, 4, 5])
+    slots, cu, lens, taken = lsx.page_map(whole[1:-1, 2:6], ints(ctx), ints(new), free, 16, 50)
+    assert done() == 0
+    assert whole[0].eq(77).all() and whole[-1].eq(77).all()
+    assert whole[:, :2].eq(77).all() and whole[:, 6:].eq(77).all()
+    assert (slots < 16 * 78).all() and free.tolist() == [3, 4, 5]
+
+
 def test_page_map_without_tokens_or_pages():
     table = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
     slots, cu, lens, taken = lsx.page_map(table, ints([0, 5]), ints([0, 0]), ints([]), 16, 0)
@@ -389,6 +405,35 @@ def test_paged_fwd_fewer_keys_than_tokens():
     assert done() == 0
     check_lse(f64(lse), l_ref, tol_lse)
     check_close(f64(o), o_ref, tol)
+
+
+@pytest.mark.parametrize("cu", [[0, 40, 20, 60], [-5, 30, 70, 1000], [60, 40, 20, 0], [0, 0, 2 ** 31 - 1, 64]])
+def test_paged_fwd_with_offsets_that_do_not_ascend(cu):
+    """Offsets are cut to the tokens there are; every row written is a row of q,
+    and the rows that one sequence alone names are its rows."""
+    q, kp, vp, table, lens, _ = prompt_case(4, 2, 64, 16, [(50, 64), (50, 64), (50, 64)])
+    t = q.shape[2] - 128
+    big = torch.full((1, 4, t + 16, 64), 7.0, device=DEV)
+    lse = torch.full((1, 4, t + 16), 7.0, device=DEV)
+    lsx.paged_fwd(q[:, :, :t], kp, vp, table, ints(lens), ints(cu), out=big[:, :, 8:-8], lse=lse[:, :, 8:-8])
+    assert done() == 0
+    assert big[:, :, :8].eq(7).all() and big[:, :, -8:].eq(7).all()
+    assert lse[:, :, :8].eq(7).all() and lse[:, :, -8:].eq(7).all()
+    cut = [min(max(c, 0), t) for c in cu]
+    named = np.zeros(t, int)
+    for a, b in zip(cut, cut[1:]):
+        named[a:b] += 1
+    tol, tol_lse = P.tolerances(q, kp, vp, P_BF16, torch.float32)
+    for i, (a, b) in enumerate(zip(cut, cut[1:])):
+        if b > a:
+            only = np.zeros(t, bool)
+            only[a:b] = named[a:b] == 1
+            fake = [0] * (i + 1) + [b - a] * (3 - i)
+            o_ref, l_ref = P.fwd(q[:, :, a:b], kp, vp, table, [n if j == i else 0 for j, n in enumerate(lens)], fake)
+            check_close(f64(big[:, :, 8:-8])[:, :, only], o_ref[:, :, only[a:b]], tol)
+            check_lse(f64(lse[:, :, 8:-8])[:, :, only], l_ref[:, :, only[a:b]], tol_lse)
+    rest = torch.from_numpy(named == 0).to(DEV)
+    assert big[:, :, 8:-8][:, :, rest].eq(7).all() and lse[:, :, 8:-8][:, :, rest].eq(7).all()
 
 
 def test_paged_fwd_equals_decode_on_single_tokens():
