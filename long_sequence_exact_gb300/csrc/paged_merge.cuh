@@ -25,6 +25,22 @@ struct RowMerge {
     constexpr float kLog2 = 1.4426950408889634f;
     for (int64_t c0 = 0; c0 < count; c0 += 32) {
       const int n = static_cast<int>(count - c0 < 32 ? count - c0 : 32);
+      float y[8][E];
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < n) {
+            const float* src = o + row_of(c0 + i0 + i) * D + lane * E;
+            if constexpr (E == 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+              y[i][0] = f.x; y[i][1] = f.y; y[i][2] = f.z; y[i][3] = f.w;
+            } else {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+              y[i][0] = f.x; y[i][1] = f.y;
+            }
+          }
+      };
+      load(0);  // (in flight while the weights are formed)
       const float mine = lane < n ? __ldcg(l + row_of(c0 + lane)) : kNone;
       float mx = mine;
 #pragma unroll
@@ -41,19 +57,7 @@ struct RowMerge {
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= keep;
       for (int i0 = 0; i0 < n; i0 += 8) {
-        float y[8][E];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < n) {
-            const float* src = o + row_of(c0 + i0 + i) * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-              y[i][0] = f.x; y[i][1] = f.y; y[i][2] = f.z; y[i][3] = f.w;
-            } else {
-              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-              y[i][0] = f.x; y[i][1] = f.y;
-            }
-          }
+        if (i0 > 0) load(i0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
