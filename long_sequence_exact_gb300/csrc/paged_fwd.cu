@@ -81,10 +81,8 @@ struct __align__(1024) Smem {
   __nv_bfloat16 v[Cfg<D>::kStages][128 * D];
   uint64_t q_full, q_empty, final_bar;
   uint64_t v_tail, v_fixed;  // the tile with a sequence's last key is in; its dead rows are cleared
-  uint64_t k_full[Cfg<D>::kStages];
-  uint64_t v_full[Cfg<D>::kStages];
-  uint64_t k_empty[Cfg<D>::kStages];
-  uint64_t v_empty[Cfg<D>::kStages];
+  uint64_t full[Cfg<D>::kStages];   // a step: K of a tile and V of the one before
+  uint64_t empty[Cfg<D>::kStages];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t item_full[kItems], item_empty[kItems];
   Item item[kItems];
@@ -200,10 +198,8 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(&sm.v_tail, 1);
     mbar_init(&sm.v_fixed, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.k_full[s], 1);
-      mbar_init(&sm.v_full[s], 1);
-      mbar_init(&sm.k_empty[s], 1);
-      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
@@ -238,7 +234,7 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- loader
       uint32_t stage = 0, phase = 0, qe_phase = 0;
-      uint32_t count = 0, k_count = 0;  // key tiles loaded; their keys
+      uint32_t count = 0, steps = 0;  // key tiles and steps loaded
       const int boxes = p.c.shift >= 7 ? 1 : 128 >> p.c.shift;  // per 64-column half
       const int rows = 128 / boxes;
       const int box = lane % boxes, sub = lane / boxes;
@@ -281,36 +277,37 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
         bool ok = true;
-        for (int j = 0; j < nkv; ++j) {
+        int v_page = 0, v_prow = 0;
+        for (int j = 0; j <= nkv && nkv > 0; ++j) {
           const int32_t mine = next;
           next = fetch(j + 1);
           const int pos = (x.e.j0 + j) * 128;
           const bool exists = mine >= 0 && mine < p.c.n_pages;
-          if (lane < 8 && !exists && pos + lane * 16 < x.e.len)
+          if (j < nkv && lane < 8 && !exists && pos + lane * 16 < x.e.len)
             atomicCAS(p.status, 0, kStatusPage);
           const uint32_t mask = __ballot_sync(0xffffffffu, exists) & 255u;
           const int page =
               __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * (8 / boxes)) & 7);
           const int prow = p.c.shift > 7 ? pos & ((1 << p.c.shift) - 1) : 0;
-          if (!wait_all(&sm.k_empty[stage], phase ^ 1)) { ok = false; break; }
+          if (!wait_all(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
           if (lane == 0) {
             // (the word of 8 tiles ago: its readers are done, for the S product
             // of the tile `stages` ago has been taken after their P)
-            *const_cast<volatile uint32_t*>(&sm.keys_ok[count % kOkRing]) = mask;
-            mbar_arrive_expect_tx(&sm.k_full[stage], C::kTileBytes);
+            if (j < nkv) *const_cast<volatile uint32_t*>(&sm.keys_ok[count % kOkRing]) = mask;
+            mbar_arrive_expect_tx(&sm.full[stage], (j > 0 && j < nkv ? 2 : 1) * C::kTileBytes);
           }
           __syncwarp();
-          if (lane < boxes * C::kSub)
-            tma_load_4d(&sm.k[stage][sub * 128 * 64 + box * rows * 64], &tm_k, &sm.k_full[stage],
-                        sub * 64, prow, x.hk, page);
-          k_count = count + 1;
-          if (!wait_all(&sm.v_empty[stage], phase ^ 1)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[stage], C::kTileBytes);
-          __syncwarp();
-          if (lane < boxes * C::kSub)
-            tma_load_4d(&sm.v[stage][sub * 128 * 64 + box * rows * 64], &tm_v, &sm.v_full[stage],
-                        sub * 64, prow, x.hk, page);
-          ++count;
+          const int at = sub * 128 * 64 + box * rows * 64;
+          if (lane < boxes * C::kSub) {
+            if (j < nkv)
+              tma_load_4d(&sm.k[stage][at], &tm_k, &sm.full[stage], sub * 64, prow, x.hk, page);
+            if (j > 0)
+              tma_load_4d(&sm.v[stage][at], &tm_v, &sm.full[stage], sub * 64, v_prow, x.hk, v_page);
+          }
+          v_page = page;
+          v_prow = prow;
+          if (j < nkv) ++count;
+          ++steps;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -318,10 +315,8 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0 && *guard.abort != 0) {
         // gave up: the copies in flight land before the block ends
         drain_wait(&sm.q_full, qe_phase ^ 1, p.wait_ns);
-        for (uint32_t i = count > kStages ? count - kStages : 0; i < k_count; ++i) {
-          drain_wait(&sm.k_full[i % kStages], (i / kStages) & 1, p.wait_ns);
-          if (i < count) drain_wait(&sm.v_full[i % kStages], (i / kStages) & 1, p.wait_ns);
-        }
+        for (uint32_t i = steps > kStages ? steps - kStages : 0; i < steps; ++i)
+          drain_wait(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------ MMA issuer
@@ -329,7 +324,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, 0, 1);
       // S_t(j+1) overwrites the columns of P_t(j); issued right after P_t(j) V_j
       // by this thread, whose products execute in order.
-      uint32_t kst = 0, kph = 0, vst = 0, vph = 0, q_phase = 0, fix_phase = 0;
+      uint32_t st = 0, ph = 0, q_phase = 0, fix_phase = 0;
       uint32_t p_phase[2] = {0, 0};
       bool issued = false;
       const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(sm.q[0]), 16, 1024),
@@ -355,28 +350,27 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         bool ok = true;
         if (nkv > 0) {  // S_t(0)
-          if (!mbar_wait(&sm.k_full[kst], kph, guard)) break;
+          if (!mbar_wait(&sm.full[st], ph, guard)) break;
           tc_fence_after();
           for (int t = 0; t < 2; ++t)
-            if ((t == 0 ? n0 : n1) > 0) issue_s(t, smem_addr(sm.k[kst]));
+            if ((t == 0 ? n0 : n1) > 0) issue_s(t, smem_addr(sm.k[st]));
           issued = true;
-          mma_commit(&sm.k_empty[kst]);
-          if (++kst == kStages) { kst = 0; kph ^= 1; }
+          mma_commit(&sm.empty[st]);
+          if (++st == kStages) { st = 0; ph ^= 1; }
         }
         // Q is free for the next item once the last S products are done
         if (nkv <= 1) mma_commit(&sm.q_empty);
         for (int j = 0; j < nkv; ++j) {
-          if (!mbar_wait(&sm.v_full[vst], vph, guard)) { ok = false; break; }
+          // V of this tile and K of the next
+          if (!mbar_wait(&sm.full[st], ph, guard)) { ok = false; break; }
           if (j == tail) {
-            sm.tail_stage = vst;
+            sm.tail_stage = st;
             mbar_arrive(&sm.v_tail);
             if (!mbar_wait(&sm.v_fixed, fix_phase, guard)) { ok = false; break; }
             fix_phase ^= 1;
           }
           tc_fence_after();
-          const uint64_t v0 = sdesc_sw128(smem_addr(sm.v[vst]), 128 * 128, 1024);
-          const bool has_next = j + 1 < nkv;
-          bool k_ready = false;
+          const uint64_t v0 = sdesc_sw128(smem_addr(sm.v[st]), 128 * 128, 1024);
           for (int t = 0; t < 2; ++t) {
             const int nt = t == 0 ? n0 : n1;
             if (j < nt) {
@@ -390,26 +384,12 @@ __global__ void __launch_bounds__(384, 1)
                        kk > 0 ? 1u : acc0);
               mma_commit(&sm.o_full[t]);
             }
-            if (has_next && j + 1 < nt) {
-              if (!k_ready) {
-                if (!mbar_wait(&sm.k_full[kst], kph, guard)) { ok = false; break; }
-                tc_fence_after();
-                k_ready = true;
-              }
-              issue_s(t, smem_addr(sm.k[kst]));
-            }
+            if (j + 1 < nt) issue_s(t, smem_addr(sm.k[st]));
           }
           if (!ok) break;
-          if (has_next) {
-            if (!k_ready) {
-              if (!mbar_wait(&sm.k_full[kst], kph, guard)) { ok = false; break; }
-            }
-            mma_commit(&sm.k_empty[kst]);
-            if (++kst == kStages) { kst = 0; kph ^= 1; }
-            if (j + 2 == nkv) mma_commit(&sm.q_empty);
-          }
-          mma_commit(&sm.v_empty[vst]);
-          if (++vst == kStages) { vst = 0; vph ^= 1; }
+          if (j + 2 == nkv) mma_commit(&sm.q_empty);
+          mma_commit(&sm.empty[st]);
+          if (++st == kStages) { st = 0; ph ^= 1; }
         }
         if (!ok) break;
       }
