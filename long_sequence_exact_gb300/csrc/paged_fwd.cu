@@ -228,9 +228,10 @@ __global__ void __launch_bounds__(384, 1)
   const int64_t n_items = item_count(p);
   const int64_t n_entries = n_items / p.Hkv;
   const int64_t grid = gridDim.x, c = blockIdx.x;
-  // registers: 128 * 104 + 256 * 200 = 64,512 = 384 * 168
+  // registers: 128 * 104 + 256 * 200 = 128 * 88 + 256 * 208 = 64,512 = 384 * 168.
+  // 32768 tokens: heads of 128 6.32 ms (88 / 208: 6.35), of 64 5.31 ms (104 / 200: 5.73)
   if (warp < 4) {
-    regs_dec<104>();
+    regs_dec<D == 64 ? 88 : 104>();
     if (warp == 0) {
       // ---------------------------------------------------------- loader
       uint32_t stage = 0, phase = 0, qe_phase = 0;
@@ -429,36 +430,38 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else {
-    regs_inc<200>();
+    regs_inc<D == 64 ? 208 : 200>();
     // ----------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2;
     const int row = threadIdx.x - 128 * (1 + t);  // 0..127 == TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + t * 128;
     const uint32_t tO = tS + 256;
-    uint32_t s_phase = 0, pv_count = 0, count = 0;
+    // The loop over key tiles holds 128 scores in registers: little else lives
+    // across it.  s_phase: parity of the s_full completions seen, which is that
+    // of the P tiles published, too.
+    uint32_t s_phase = 0;
+    uint32_t tile = 0;  // key tiles taken (by either query tile), for keys_ok
     const float sl2 = p.scale_log2;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return mbar_wait(bar, parity, WaitGuard{p.status, p.wait_ns, &sm.abort});
     };
     for (uint32_t r = 0;; ++r) {
       if (!wait(&sm.item_full[r % kItems], (r / kItems) & 1)) break;
-      int nkv, kb, lim, lim_tile, tiles;
+      int left, last;  // key tiles left; the row's last key within the next one
       {
         const Item& x = sm.item[r % kItems];
         if (x.hk < 0) break;
-        nkv = x.n[t];
-        tiles = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
-        kb = x.e.j0 * 128;
-        lim = last_key(p, x.e, t * p.tpt + row / p.per);
-        lim_tile = last_key(p, x.e, t * p.tpt);
+        left = x.n[t];
+        last = last_key(p, x.e, t * p.tpt + row / p.per) - x.e.j0 * 128;
       }
       float m = kNegInf, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < nkv; ++j, kb += 128) {
+      bool ok = true, first = true;
+      for (; left > 0; --left, ++tile, last -= 128) {
         if (!wait(&sm.s_full[t], s_phase)) { ok = false; break; }
         s_phase ^= 1;
         tc_fence_after();
+        const uint32_t okm = *const_cast<volatile uint32_t*>(&sm.keys_ok[tile % kOkRing]);
         float s[128];
         {
           uint32_t u0[32], u1[32], u2[32], u3[32];
@@ -478,13 +481,11 @@ __global__ void __launch_bounds__(384, 1)
             s[96 + i] = __uint_as_float(u3[i]);
           }
         }
-        if (kb + 127 > lim_tile) {
-          const int last = lim - kb;
+        if (last < 127) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i > last) s[i] = kNegInf;
         }
-        const uint32_t okm = *const_cast<volatile uint32_t*>(&sm.keys_ok[(count + j) % kOkRing]);
         if (okm != 255u) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -502,13 +503,14 @@ __global__ void __launch_bounds__(384, 1)
         mx1 = fmax3(mx1, s[126], s[127]);
         const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
         const float m_new = fmaxf(m, mx * sl2);
-        if (j == 0) {
+        if (first) {
           m = m_new;
+          first = false;
         } else {
           const bool need = m_new > m + kRescaleThreshold;
           if (__any_sync(0xffffffffu, need)) {
             // O_t must hold the finished P_t V of the previous key tile
-            if (!wait(&sm.o_full[t], (pv_count - 1) & 1)) { ok = false; break; }
+            if (!wait(&sm.o_full[t], s_phase)) { ok = false; break; }
             tc_fence_after();
             const float alpha = (m == kNegInf) ? 0.f : ex2(m - m_new);
 #pragma unroll
@@ -547,16 +549,16 @@ __global__ void __launch_bounds__(384, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[t]);
-        ++pv_count;
       }
       if (!ok) break;
-      count += tiles;
       // ------------------------------------------------------- epilogue
       const Item& x = sm.item[r % kItems];
+      const int nkv = x.n[t];
+      if (x.n[1 - t] > nkv) tile += x.n[1 - t] - nkv;
       const int tok = row / p.per, rem = row - tok * p.per;
       const bool valid = tok < tile_tokens(p, x.e, t);
       if (nkv > 0) {
-        if (!wait(&sm.o_full[t], (pv_count - 1) & 1)) break;
+        if (!wait(&sm.o_full[t], s_phase ^ 1)) break;
         tc_fence_after();
       }
       const float inv = (l > 0.f) ? 1.f / l : 0.f;
