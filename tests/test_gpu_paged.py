@@ -561,6 +561,50 @@ def test_calls_on_another_stream_wait_for_nothing_else():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_views_of_a_fused_projection():
+    """q, k and v as slices of one projection row: strides wider than the heads,
+    results in q's order of dimensions, the same bits as from dense copies."""
+    hq, hkv, d, page, new = 6, 2, 64, 16, [40, 3, 70]
+    qkv = random_tensor((sum(new), (hq + 2 * hkv) * d), 8, device=DEV)
+    q = qkv[:, :hq * d].view(-1, hq, d).transpose(0, 1)[None]
+    k = qkv[:, hq * d:(hq + hkv) * d].view(-1, hkv, d).transpose(0, 1)[None]
+    v = qkv[:, (hq + hkv) * d:].view(-1, hkv, d).transpose(0, 1)[None]
+    kp, vp = pool(12, hkv, page, d, 1), pool(12, hkv, page, d, 2, token_major=False)
+    table = torch.full((3, 8), -1, dtype=torch.int32, device=DEV)
+    slots, cu, lens, _ = lsx.page_map(table, ints([0, 0, 0]), ints(new), ints(list(range(12))), page, sum(new))
+    lsx.page_append(k, v, kp, vp, slots)
+    kd, vd = kp.clone(), vp.clone()
+    lsx.page_append(k.contiguous(), v.contiguous(), kd, vd, slots)
+    o, lse = lsx.paged_fwd(q, kp, vp, table, lens, cu)
+    o2, lse2 = lsx.paged_fwd(q.contiguous(), kp, vp, table, lens, cu)
+    last = [int(x) - 1 for x in cu[1:]]
+    q1 = q[0, :, last].transpose(0, 1)[:, :, None]   # [3, Hq, 1, D], one token a sequence
+    wide = torch.stack([qkv[i] for i in last])[:, :hq * d].view(3, hq, 1, d)
+    o3, lse3 = lsx.paged_decode(wide, kp, vp, table, lens)
+    o4, lse4 = lsx.paged_decode(q1.contiguous(), kp, vp, table, lens)
+    assert done() == 0
+    assert torch.equal(kp, kd) and torch.equal(vp, vd)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert torch.equal(o3, o4) and torch.equal(lse3, lse4)
+    assert o[0].transpose(0, 1).is_contiguous()
+
+
+def test_first_call_of_a_variant_inside_a_capture():
+    """Captured without a call before it (heads of 64, 64 rows a key head; 100 heads a key head)."""
+    q, kp, vp, table, _ = decode_case(64, 1, 1, 64, 32, [300, 9], 0, seed=77, width=2000)
+    lens = ints([300, 9])
+    qq, kq, vq, tq, lq, cq = prompt_case(100, 1, 64, 32, [(5, 7), (0, 30)], seed=78)
+    args = (qq, kq, vq, tq, ints(lq), ints(cq))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = lsx.paged_decode(q, kp, vp, table, lens) + lsx.paged_fwd(*args)
+    g.replay()
+    want = lsx.paged_decode(q, kp, vp, table, lens) + lsx.paged_fwd(*args)
+    assert done() == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
 def test_python_refusals():
     q, kp, vp, table, _ = decode_case(4, 2, 1, 128, 16, [50, 3], 0)
     lens = ints([50, 3])
