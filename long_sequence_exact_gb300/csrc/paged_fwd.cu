@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(384, 1)
       bool issued = false;
       const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(sm.q[0]), 16, 1024),
                                   sdesc_sw128(smem_addr(sm.q[1]), 16, 1024)};
-      auto issue_s = [&](int t, uint32_t k_addr) {
-        const uint64_t k0 = sdesc_sw128(k_addr, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_addr(sm.k[0]), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_addr(sm.v[0]), 128 * 128, 1024);
+      auto issue_s = [&](int t, uint32_t stage) {
+        const uint64_t k0 = k_desc + stage * (C::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(tmem + t * 128, q_desc[t] + kmajor_step(kk, 128), k0 + kmajor_step(kk, 128),
@@ -364,14 +366,37 @@ __global__ void __launch_bounds__(384, 1)
           if (!mbar_wait(&sm.full[st], ph, guard)) break;
           tc_fence_after();
           for (int t = 0; t < 2; ++t)
-            if ((t == 0 ? n0 : n1) > 0) issue_s(t, smem_addr(sm.k[st]));
+            if ((t == 0 ? n0 : n1) > 0) issue_s(t, st);
           issued = true;
           mma_commit(&sm.empty[st]);
           if (++st == kStages) { st = 0; ph ^= 1; }
         }
         // Q is free for the next item once the last S products are done
         if (nkv <= 1) mma_commit(&sm.q_empty);
-        for (int j = 0; j < nkv; ++j) {
+        int j = 0;
+        for (const int both = (n0 < n1 ? n0 : n1) - 2; j < both; ++j) {
+          // (both query tiles take this tile and the next two: no conditions)
+          if (!mbar_wait(&sm.full[st], ph, guard)) { ok = false; break; }
+          const uint64_t v0 = v_desc + st * (C::kTileBytes >> 4);
+          const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!mbar_wait(&sm.p_full[t], p_phase[t], guard)) { ok = false; break; }
+            p_phase[t] ^= 1;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v0 + mnmajor_step(kk), kIdO,
+                     kk > 0 ? 1u : acc0);
+            mma_commit(&sm.o_full[t]);
+            issue_s(t, st);
+          }
+          if (!ok) break;
+          mma_commit(&sm.empty[st]);
+          if (++st == kStages) { st = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        for (; j < nkv; ++j) {
           // V of this tile and K of the next
           if (!mbar_wait(&sm.full[st], ph, guard)) { ok = false; break; }
           if (j == tail) {
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(384, 1)
             fix_phase ^= 1;
           }
           tc_fence_after();
-          const uint64_t v0 = sdesc_sw128(smem_addr(sm.v[st]), 128 * 128, 1024);
+          const uint64_t v0 = v_desc + st * (C::kTileBytes >> 4);
           for (int t = 0; t < 2; ++t) {
             const int nt = t == 0 ? n0 : n1;
             if (j < nt) {
@@ -395,7 +420,7 @@ __global__ void __launch_bounds__(384, 1)
                        kk > 0 ? 1u : acc0);
               mma_commit(&sm.o_full[t]);
             }
-            if (j + 1 < nt) issue_s(t, smem_addr(sm.k[st]));
+            if (j + 1 < nt) issue_s(t, st);
           }
           if (!ok) break;
           if (j + 2 == nkv) mma_commit(&sm.q_empty);
