@@ -385,9 +385,11 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *   its keys j <= kv_len - Nq + n (the Nq tokens are its last ones).
  *   prefix_table: int32, the pages of prefix_len keys that every query sees
  *   before its own (NULL when prefix_len is 0): a prefix shared by the batch,
- *   read once for up to 64 query rows together, not once per sequence.
+ *   read once for up to 256 query rows together, not once per sequence.
  *   o [B, Hq, Nq, D] bf16 or f32, lse [B, Hq, Nq, 1] f32; a query without
- *   keys gets O = 0, LSE = -inf.  P is kept to 16 bits in the P V product.
+ *   keys gets O = 0, LSE = -inf.  P is kept to 16 bits in the P V product; that
+ *   of a prefix which more than 32 query rows of a kv head share, B * (Hq / Hkv)
+ *   * Nq, is rounded to bf16.
  *
  * attn_paged_fwd -- prompts: ragged query tokens, causal, over the cache.
  *   q [1, Hq, T, D] bf16, the tokens of sequence b at [cu_q[b], cu_q[b + 1])

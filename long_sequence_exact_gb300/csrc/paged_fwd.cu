@@ -6,9 +6,9 @@
 //
 // Bound: the tensor cores (4 D operations per visible (query, key) pair), for
 // few tokens the cache's bytes.  32 query and 8 kv heads of 128: 12345 tokens
-// 0.92 ms, 1.36 PFLOP/s; 32768 tokens 6.33 ms, 1.39 PFLOP/s; 512 tokens after 65536
-// keys 0.436 ms, of which the partials' merge 0.015; heads of 64, 32768 tokens
-// 5.26 ms, 0.84 PFLOP/s.
+// 0.776 ms, 1.61 PFLOP/s; 32768 tokens 5.54 ms, 1.59 PFLOP/s; 512 tokens after 65536
+// keys 0.390 ms, of which the partials' merge 0.015; heads of 64, 32768 tokens
+// 4.35 ms, 1.01 PFLOP/s.
 //
 // Rows.  The heads that share a key head are rows of one tile: row r of a
 // 128-row query tile is head r % G of token r / G, floor(128 / G) tokens a tile,
@@ -30,12 +30,27 @@
 // replaces S_t.  The MMA order per key tile j is P_0 V_j, S_0(j+1), P_1 V_j,
 // S_1(j+1): each tile's softmax runs under two products of the other.
 //
-// The issuing thread sets the pace: every barrier that it looks at costs it
-// about 150 cycles, of some 3,700 a key tile.  So what it consumes together
-// arrives together: a step of the ring holds V of tile j and K of tile j + 1,
-// one barrier when both are in and one when both are free (tokens 12345: 980 us
-// with barriers of their own, 928 us so).  Publishing P in halves, with one
-// wait more, costs 7%.
+// The issuing thread and the softmax take turns in setting the pace, so both are
+// kept short (times of the 12345 tokens above, one after the other):
+// - What is consumed together arrives together: a step of the ring holds V of
+//   tile j and K of tile j + 1, one barrier when both are in and one when both
+//   are free; a barrier looked at costs the issuing thread about 150 cycles
+//   (980 -> 928 us).
+// - The tiles that both query tiles take go through a loop without conditions,
+//   descriptors move by their low words (919 -> 833 us).
+// - The softmax takes no maximum of a tile as a rule (833 -> 789 us, heads of 64
+//   5.0 -> 4.3 ms at 32768 tokens): the weights exp2(s - m) of any m give the same
+//   quotient as long as they neither overflow nor vanish.  m starts at 0; where a
+//   row's sum leaves [2^-32, 2^32] the tile's maximum is formed, m moved to the size
+//   of the sum, O rescaled and the tile's weights formed again.  Rows that end in
+//   their first tile take its maximum all the same: their largest weight is then
+//   exactly 1, and a row with one key is that key's value.
+// - Query tile 1's first scores wait for tile 0's first softmax: the two stay out
+//   of step, each softmax under the other's products (789 -> 776 us).
+// Measured and not kept: P published in halves (a wait more: +7%, and nothing
+// once the rest was short), O's barrier once per item (+2%), scores read from
+// TMEM in parts between the exponentials (+7% to +14%), the next tile prefetched
+// into L2 (+1% to +50%; -3% where a prefix streams from HBM).
 //
 // Pages.  A tile of 128 keys is 128 / page boxes of a page each (one for pages
 // of 128 and more).  A page past the length or one that does not exist is
@@ -57,11 +72,12 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // base 2: P <= 256 under a stale maximum
-constexpr int kOkRing = 8;                 // >= stages + 2 (see the loader)
-constexpr int kItems = 4;                  // items handed to the other roles ahead
-constexpr int kMinPiece = 4;               // key tiles
-constexpr int kPiecesPerSm = 4;            // at most, over all units and kv heads
+constexpr float kMostSum = 4294967296.f;     // 2^32 (see the softmax)
+constexpr float kLeastSum = 2.3283064e-10f;  // 2^-32
+constexpr int kOkRing = 8;       // >= stages + 2 (see the loader)
+constexpr int kItems = 4;        // items handed to the other roles ahead
+constexpr int kMinPiece = 4;     // key tiles
+constexpr int kPiecesPerSm = 4;  // at most, over all units and kv heads
 constexpr int kPlanThreads = 512;
 
 // What a CTA works on: tokens [tok0, tok0 + ntok) of sequence b (rows of up to
@@ -177,6 +193,29 @@ __device__ __forceinline__ int tail_tile(const FwdParams& p, const Entry& e, int
   if ((e.len & ((1 << p.c.shift) - 1)) == 0) return -1;
   const int j = (e.len >> 7) - e.j0;
   return j >= 0 && j < nkv ? j : -1;
+}
+
+// The products with the low word of a descriptor given apart: the step along K is
+// added to it alone (the address field does not carry out of it).
+__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -338,17 +377,31 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t st = 0, ph = 0, q_phase = 0, fix_phase = 0;
       uint32_t p_phase[2] = {0, 0};
       bool issued = false;
-      const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(sm.q[0]), 16, 1024),
-                                  sdesc_sw128(smem_addr(sm.q[1]), 16, 1024)};
-      const uint64_t k_desc = sdesc_sw128(smem_addr(sm.k[0]), 16, 1024);
+      // operand descriptors: the low words move, with the tile and the step along K
+      constexpr uint32_t kTileDesc = C::kTileBytes >> 4;
+      const uint64_t q_desc = sdesc_sw128(smem_addr(sm.q[0]), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_addr(sm.v[0]), 128 * 128, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc);
+      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(smem_addr(sm.k[0]), 16, 1024));
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc);
+      const uint32_t qk_hi = static_cast<uint32_t>(q_desc >> 32);
+      const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
       auto issue_s = [&](int t, uint32_t stage) {
-        const uint64_t k0 = k_desc + stage * (C::kTileBytes >> 4);
+        const uint32_t q0 = q_lo + t * kTileDesc, k0 = k_lo + stage * kTileDesc;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + t * 128, q_desc[t] + kmajor_step(kk, 128), k0 + kmajor_step(kk, 128),
-                 kIdS, kk > 0 ? 1u : 0u);
+          mma_ss_lo(tmem + t * 128, q0 + static_cast<uint32_t>(kmajor_step(kk, 128)), qk_hi,
+                    k0 + static_cast<uint32_t>(kmajor_step(kk, 128)), qk_hi, kIdS,
+                    kk > 0 ? 1u : 0u);
         mma_commit(&sm.s_full[t]);
+      };
+      auto issue_pv = [&](int t, uint32_t stage, uint32_t acc0) {
+        const uint32_t v0 = v_lo + stage * kTileDesc;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_lo(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                    v0 + static_cast<uint32_t>(mnmajor_step(kk)), v_hi, kIdO, kk > 0 ? 1u : acc0);
+        mma_commit(&sm.o_full[t]);
       };
       for (uint32_t r = 0;; ++r) {
         if (!mbar_wait(&sm.item_full[r % kItems], (r / kItems) & 1, guard)) break;
@@ -365,9 +418,11 @@ __global__ void __launch_bounds__(384, 1)
         if (nkv > 0) {  // S_t(0)
           if (!mbar_wait(&sm.full[st], ph, guard)) break;
           tc_fence_after();
-          for (int t = 0; t < 2; ++t)
-            if ((t == 0 ? n0 : n1) > 0) issue_s(t, st);
+          if (n0 > 0) issue_s(0, st);
           issued = true;
+          // the other tile's scores once this one's softmax is done
+          if (n0 > 1 && n1 > 1 && !mbar_wait(&sm.p_full[0], p_phase[0], guard)) break;
+          if (n1 > 0) issue_s(1, st);
           mma_commit(&sm.empty[st]);
           if (++st == kStages) { st = 0; ph ^= 1; }
         }
@@ -375,20 +430,14 @@ __global__ void __launch_bounds__(384, 1)
         if (nkv <= 1) mma_commit(&sm.q_empty);
         int j = 0;
         for (const int both = (n0 < n1 ? n0 : n1) - 2; j < both; ++j) {
-          // (both query tiles take this tile and the next two: no conditions)
+          // both query tiles take this tile and the next two: no conditions
           if (!mbar_wait(&sm.full[st], ph, guard)) { ok = false; break; }
-          const uint64_t v0 = v_desc + st * (C::kTileBytes >> 4);
-          const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!mbar_wait(&sm.p_full[t], p_phase[t], guard)) { ok = false; break; }
             p_phase[t] ^= 1;
             tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v0 + mnmajor_step(kk), kIdO,
-                     kk > 0 ? 1u : acc0);
-            mma_commit(&sm.o_full[t]);
+            issue_pv(t, st, j > 0 ? 1u : 0u);
             issue_s(t, st);
           }
           if (!ok) break;
@@ -406,19 +455,13 @@ __global__ void __launch_bounds__(384, 1)
             fix_phase ^= 1;
           }
           tc_fence_after();
-          const uint64_t v0 = v_desc + st * (C::kTileBytes >> 4);
           for (int t = 0; t < 2; ++t) {
             const int nt = t == 0 ? n0 : n1;
             if (j < nt) {
               if (!mbar_wait(&sm.p_full[t], p_phase[t], guard)) { ok = false; break; }
               p_phase[t] ^= 1;
               tc_fence_after();
-              const uint32_t acc0 = j > 0 ? 1u : 0u;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, v0 + mnmajor_step(kk), kIdO,
-                       kk > 0 ? 1u : acc0);
-              mma_commit(&sm.o_full[t]);
+              issue_pv(t, st, j > 0 ? 1u : 0u);
             }
             if (j + 1 < nt) issue_s(t, st);
           }
@@ -472,9 +515,10 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + t * 128;
     const uint32_t tO = tS + 256;
-    // The loop over key tiles holds 128 scores in registers: little else lives
-    // across it.  s_phase: parity of the s_full completions seen, which is that
-    // of the P tiles published, too.
+    // The loop over key tiles holds 128 scores in registers (to the end: their
+    // weights may have to be formed again): little else lives across it.  s_phase:
+    // parity of the s_full completions seen, which is that of the P tiles
+    // published, too.  live: a row that is written (others may hold anything).
     uint32_t s_phase = 0;
     uint32_t tile = 0;  // key tiles taken (by either query tile), for keys_ok
     const float sl2 = p.scale_log2;
@@ -484,13 +528,15 @@ __global__ void __launch_bounds__(384, 1)
     for (uint32_t r = 0;; ++r) {
       if (!wait(&sm.item_full[r % kItems], (r / kItems) & 1)) break;
       int left, last;  // key tiles left; the row's last key within the next one
+      bool live;
       {
         const Item& x = sm.item[r % kItems];
         if (x.hk < 0) break;
         left = x.n[t];
         last = last_key(p, x.e, t * p.tpt + row / p.per) - x.e.j0 * 128;
+        live = row / p.per < tile_tokens(p, x.e, t);
       }
-      float m = kNegInf, l = 0.f;
+      float m = 0.f, l = 0.f;
       bool ok = true, first = true;
       for (; left > 0; --left, ++tile, last -= 128) {
         if (!wait(&sm.s_full[t], s_phase)) { ok = false; break; }
@@ -526,28 +572,47 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 128; ++i)
             if (((okm >> (i / 16)) & 1u) == 0) s[i] = kNegInf;
         }
-        float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+        auto weights = [&]() -> float {
+          const float2 sc2 = make_float2(sl2, sl2);
+          const float2 nm2 = make_float2(-m, -m);
+          float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 4; i < 124; i += 8) {
-          mx0 = fmax3(mx0, s[i], s[i + 1]);
-          mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
-          mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
-          mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
-        }
-        mx0 = fmax3(mx0, s[124], s[125]);
-        mx1 = fmax3(mx1, s[126], s[127]);
-        const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
-        const float m_new = fmaxf(m, mx * sl2);
-        if (first) {
-          m = m_new;
-          first = false;
-        } else {
-          const bool need = m_new > m + kRescaleThreshold;
-          if (__any_sync(0xffffffffu, need)) {
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 arg =
+                  __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
+              const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
+              if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
+              pk[i] = pack_bf16(e.x, e.y);
+            }
+            tmem_st16(tS + cc * 16, pk);
+          }
+          return (la.x + la.y) + (lb.x + lb.y);
+        };
+        float part = weights();  // the tile's row sum under m
+        const bool few = first && last < 127;  // the row ends in this tile
+        if (__any_sync(0xffffffffu, live && (few || !(part < kMostSum && l + part > kLeastSum)))) {
+          float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+          for (int i = 4; i < 124; i += 8) {
+            mx0 = fmax3(mx0, s[i], s[i + 1]);
+            mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
+            mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
+            mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
+          }
+          mx0 = fmax3(mx0, s[124], s[125]);
+          mx1 = fmax3(mx1, s[126], s[127]);
+          const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+          // m to the size of what the row has, or gets: alpha is at most 1 / l
+          float m_new = fmaxf(l > 0.f ? m + lg2(l) : kNegInf, mx * sl2);
+          if (!(m_new > kNegInf)) m_new = m;
+          if (!first) {
             // O_t must hold the finished P_t V of the previous key tile
             if (!wait(&sm.o_full[t], s_phase)) { ok = false; break; }
             tc_fence_after();
-            const float alpha = (m == kNegInf) ? 0.f : ex2(m - m_new);
+            const float alpha = l > 0.f ? ex2(m - m_new) : 0.f;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
               uint32_t u[32];
@@ -560,27 +625,12 @@ __global__ void __launch_bounds__(384, 1)
             }
             tmem_st_wait();
             l *= alpha;
-            m = m_new;
           }
+          m = m_new;
+          part = weights();
         }
-        const float mu = (m == kNegInf) ? 0.f : m;
-        const float2 sc2 = make_float2(sl2, sl2);
-        const float2 nm2 = make_float2(-mu, -mu);
-        float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 arg =
-                __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
-            const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
-            if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
-            pk[i] = pack_bf16(e.x, e.y);
-          }
-          tmem_st16(tS + cc * 16, pk);
-        }
-        l += (la.x + la.y) + (lb.x + lb.y);
+        l += part;
+        first = false;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[t]);

@@ -102,15 +102,15 @@ def score_error(q, k, scale=None):
 
 
 def tolerances(q, kp, vp, p_rounding, out_dtype, scale=None):
-    """(O, LSE) bounds.  A weight p_j = exp(s_j - m) is off by e_s (its score)
-    + 2^-21 (base-2 exponential, its fp32 argument up to 8 bits above the point)
-    + p_rounding relative, numerator and denominator each, fp32 sums add a few
-    2^-24 * sqrt(n) (taken as 2^-19): |dO| <= 2 (..) max|v|, and a bf16 output
-    half a step of |O| <= max|v|.  |dLSE| <= e_s + 2^-21 + 2^-19 plus fp32
-    rounding of an LSE below 64 (2^-19)."""
+    """(O, LSE) bounds.  A weight p_j = exp2(s_j - m) is off by e_s (its score),
+    2^-19 (the fp32 argument, below 2^5: half a step of it) and 2^-21 (the
+    exponential), and by p_rounding relative in the numerator; fp32 sums add a few
+    2^-24 * sqrt(n) (taken as 2^-19): |dO| <= (2 (..) + p_rounding) max|v|, and a
+    bf16 output half a step of |O| <= max|v|.  |dLSE| <= those, plus fp32 rounding
+    of an LSE below 64 (2^-19)."""
     es = score_error(q, kp, scale)
     vmax = float(vp.float().abs().max())
-    rel = es + 2.0 ** -21 + 2.0 ** -19
+    rel = es + 2.0 ** -19 + 2.0 ** -21 + 2.0 ** -19
     tol = (2 * rel + p_rounding) * vmax
     if out_dtype == torch.bfloat16:
         tol += U16 * vmax
