@@ -22,10 +22,11 @@
 // and merge reads cost least (plan_kernel, from the lengths on the device).
 // A cut unit leaves fp32 partials (O, LSE), merged by the LSE rule at the end.
 //
-// CTA roles (384 threads, one CTA an SM): warp 0 loads (TMA; one lane per
-// page and 64-column half) and hands the decoded items on, warp 1 lane 0 issues
-// the MMAs, warp 2 clears the value rows past a sequence's last key, warps 4..7
-// and 8..11 do the softmax of query tile 0 and 1 (thread = row = TMEM lane).
+// CTA roles (384 threads, one CTA an SM): warp 0 loads queries and keys and hands
+// the decoded items on, warp 3 loads values (TMA, one lane per page and 64-column
+// half), warp 1 lane 0 issues the MMAs, warp 2 clears the value rows past a
+// sequence's last key, warps 4..7 and 8..11 do the softmax of query tile 0 and 1
+// (thread = row = TMEM lane).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D); P_t (bf16)
 // replaces S_t.  The MMA order per key tile j is P_0 V_j, S_0(j+1), P_1 V_j,
 // S_1(j+1): each tile's softmax runs under two products of the other.
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], 10);  // MMA thread, clearing warp, 8 softmax warps
+      mbar_init(&sm.item_empty[i], 11);  // MMA thread, warps 2 and 3, 8 softmax warps
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.s_full[t], 1);
@@ -281,19 +282,35 @@ __global__ void __launch_bounds__(384, 1)
   // 32768 tokens: heads of 128 6.32 ms (88 / 208: 6.35), of 64 5.31 ms (104 / 200: 5.73)
   if (warp < 4) {
     regs_dec<D == 64 ? 88 : 104>();
+    // Loads: a box per page and 64-column half, each from a lane of its own; the
+    // 16-key groups of a tile are in lanes 0..7, a tile ahead.
+    const int boxes = p.c.shift >= 7 ? 1 : 128 >> p.c.shift;  // per 64-column half
+    const int rows = 128 / boxes;
+    const int box = lane % boxes, sub = lane / boxes;
+    const int at = sub * 128 * 64 + box * rows * 64;  // where it goes in a tile
+    auto group_page = [&](const Item& x, int j, int nkv) -> int32_t {
+      const int pos = (x.e.j0 + j) * 128 + lane * 16;
+      return j < nkv && lane < 8 && pos < x.e.len
+                 ? __ldg(p.c.table + x.e.b * p.c.table_stride + (pos >> p.c.shift))
+                 : -1;
+    };
+    auto box_page = [&](int32_t mine) {
+      const bool exists = mine >= 0 && mine < p.c.n_pages;
+      return __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * (8 / boxes)) & 7);
+    };
+    auto page_row = [&](const Item& x, int j) {
+      return p.c.shift > 7 ? (x.e.j0 + j) * 128 & ((1 << p.c.shift) - 1) : 0;
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(bar, parity, guard);
+      return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
     if (warp == 0) {
-      // ---------------------------------------------------------- loader
+      // --------------------------------------- items, queries and keys
       uint32_t stage = 0, phase = 0, qe_phase = 0;
       uint32_t count = 0, steps = 0;  // key tiles and steps loaded
-      const int boxes = p.c.shift >= 7 ? 1 : 128 >> p.c.shift;  // per 64-column half
-      const int rows = 128 / boxes;
-      const int box = lane % boxes, sub = lane / boxes;
       const uint32_t q_bytes = 2 * C::kSub * p.per * p.tpt * 128;
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(bar, parity, guard);
-        return __shfl_sync(0xffffffffu, ok, 0) != 0;
-      };
       for (int64_t r = 0;; ++r) {
         // (decoded here, ahead of time, and handed to the other roles in a slot)
         const int64_t it = snake_item(c, r, grid);
@@ -308,13 +325,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (x.hk < 0) break;
         const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
-        // page of each 16-key group of a tile in lanes 0..7, a tile ahead
-        const int32_t* row = p.c.table + x.e.b * p.c.table_stride;
-        auto fetch = [&](int j) -> int32_t {
-          const int pos = (x.e.j0 + j) * 128 + lane * 16;
-          return j < nkv && lane < 8 && pos < x.e.len ? __ldg(row + (pos >> p.c.shift)) : -1;
-        };
-        int32_t next = fetch(0);
+        int32_t next = group_page(x, 0, nkv);
         if (!wait_all(&sm.q_empty, qe_phase ^ 1)) break;
         qe_phase ^= 1;
         if (lane == 0) {
@@ -327,18 +338,14 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
         bool ok = true;
-        int v_page = 0, v_prow = 0;
-        for (int j = 0; j <= nkv && nkv > 0; ++j) {
+        for (int j = 0; j <= nkv && nkv > 0; ++j) {  // step j: K of tile j, V of tile j - 1
           const int32_t mine = next;
-          next = fetch(j + 1);
-          const int pos = (x.e.j0 + j) * 128;
+          next = group_page(x, j + 1, nkv);
           const bool exists = mine >= 0 && mine < p.c.n_pages;
-          if (j < nkv && lane < 8 && !exists && pos + lane * 16 < x.e.len)
+          if (j < nkv && lane < 8 && !exists && (x.e.j0 + j) * 128 + lane * 16 < x.e.len)
             atomicCAS(p.status, 0, kStatusPage);
           const uint32_t mask = __ballot_sync(0xffffffffu, exists) & 255u;
-          const int page =
-              __shfl_sync(0xffffffffu, exists ? mine : p.c.n_pages, (box * (8 / boxes)) & 7);
-          const int prow = p.c.shift > 7 ? pos & ((1 << p.c.shift) - 1) : 0;
+          const int page = box_page(mine);
           if (!wait_all(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
           if (lane == 0) {
             // (the word of 8 tiles ago: its readers are done, for the S product
@@ -347,15 +354,9 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(&sm.full[stage], (j > 0 && j < nkv ? 2 : 1) * C::kTileBytes);
           }
           __syncwarp();
-          const int at = sub * 128 * 64 + box * rows * 64;
-          if (lane < boxes * C::kSub) {
-            if (j < nkv)
-              tma_load_4d(&sm.k[stage][at], &tm_k, &sm.full[stage], sub * 64, prow, x.hk, page);
-            if (j > 0)
-              tma_load_4d(&sm.v[stage][at], &tm_v, &sm.full[stage], sub * 64, v_prow, x.hk, v_page);
-          }
-          v_page = page;
-          v_prow = prow;
+          if (j < nkv && lane < boxes * C::kSub)
+            tma_load_4d(&sm.k[stage][at], &tm_k, &sm.full[stage], sub * 64, page_row(x, j), x.hk,
+                        page);
           if (j < nkv) ++count;
           ++steps;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -367,6 +368,32 @@ __global__ void __launch_bounds__(384, 1)
         drain_wait(&sm.q_full, qe_phase ^ 1, p.wait_ns);
         for (uint32_t i = steps > kStages ? steps - kStages : 0; i < steps; ++i)
           drain_wait(&sm.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+      }
+    } else if (warp == 3) {
+      // ----------------------------------------------------------- values
+      // (the step's barrier is armed for both tiles by warp 0)
+      uint32_t stage = 0, phase = 0;
+      for (uint32_t r = 0;; ++r) {
+        if (!wait_all(&sm.item_full[r % kItems], (r / kItems) & 1)) break;
+        const Item x = sm.item[r % kItems];
+        if (x.hk < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[r % kItems]);
+        const int nkv = x.n[0] > x.n[1] ? x.n[0] : x.n[1];
+        int32_t next = group_page(x, 0, nkv);
+        bool ok = true;
+        for (int j = 0; j <= nkv && nkv > 0; ++j) {
+          if (j > 0) {
+            const int page = box_page(next);
+            next = group_page(x, j, nkv);
+            if (!wait_all(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
+            if (lane < boxes * C::kSub)
+              tma_load_4d(&sm.v[stage][at], &tm_v, &sm.full[stage], sub * 64, page_row(x, j - 1),
+                          x.hk, page);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------ MMA issuer
