@@ -7,14 +7,13 @@
 // up to 64 query rows (heads of its group x query tokens) that need it.
 //
 // Decomposition.  A unit is (sequence, kv head): R = (Hq / Hkv) * Nq query
-// rows against that sequence's keys, in steps of 64 keys.  The steps of all
-// units, laid end to end, are cut into equal runs, one per CTA (two CTAs an
-// SM), whatever the lengths are: no CTA has more than one step more than
-// another.  A run that covers a unit whole writes its result; a unit cut
-// between runs leaves normalised partials (fp32 O, LSE) in the workspace, at
-// most two per CTA, and the merge kernel, launched while the first one still
-// runs, combines them by the LSE rule in the order of the keys.  Which run
-// holds what follows from the lengths alone, which every CTA sums for itself.
+// rows against that sequence's keys, in steps of 64 or 128 keys.  The steps of all
+// units, laid end to end, are cut into runs of equal cost, one per CTA (two CTAs
+// an SM), whatever the lengths are.  A run that covers a unit whole writes its
+// result; a unit cut between runs leaves normalised partials (fp32 O, LSE) in the
+// workspace, at most two per CTA, and the merge kernel, launched while the first
+// one still runs, combines them by the LSE rule in the order of the keys.  Which
+// run holds what follows from the lengths alone, which every CTA sums for itself.
 //
 // A step is 16 KB of keys and 16 KB of values (64 keys of 128, 128 keys of 64),
 // loaded page by page with TMA into one of three stages by a warp of its own,
@@ -70,7 +69,7 @@ struct PagedDecodeParams {
   int64_t whole_slot0;  // ... or leaves it in this slot + the unit's number
   lsx_tensor o, lse;
   PartView part;
-  int64_t* start;       // [units_b + 1] first step of each, per kv head
+  int64_t* start;       // [units_b + 1] steps before each, per kv head
   int* status;
   uint64_t wait_ns;
 };

@@ -136,6 +136,7 @@ struct FwdParams {
   int32_t u_tokens, u_len, u_pieces, u_size;
   float scale_log2;
   lsx_tensor o, lse;
+  bool wide;      // the rows of o are 32-byte aligned
   float* part_o;  // [slot][Hkv][256][D]
   float* part_l;  // [slot][Hkv][256]
   int* status;
@@ -217,6 +218,24 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// N words of a row, 32 bytes a store (16 where the row is only so aligned).
+template <int N>
+__device__ __forceinline__ void store_row(void* dst, const uint32_t (&w)[N], bool wide) {
+  uint32_t* p = static_cast<uint32_t*>(dst);
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i),
+                   "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                   "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -680,6 +699,8 @@ __global__ void __launch_bounds__(384, 1)
           (static_cast<int64_t>(x.e.slot) * p.Hkv + x.hk) * 256 + t * 128 + row;
       const int64_t token = x.e.tok0 + t * p.tpt + tok;
       const int64_t h = static_cast<int64_t>(x.hk) * p.G + rem;  // (direct: rem is the head)
+      // 32-byte stores where the rows allow it: a whole sector per lane and store
+      const bool wide = part || p.wide;
       float* f32 = part ? p.part_o + prow * D
                         : (p.o.dtype == LSX_F32
                                ? static_cast<float*>(p.o.data) + view_off(p.o, 0, h, token)
@@ -700,16 +721,15 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) ov[i] = l > 0.f ? __uint_as_float(u[i]) * inv : 0.f;
         if (f32 != nullptr) {
+          uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(f32 + cc * 32 + i) =
-                make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(ov[i]);
+          store_row(f32 + cc * 32, w, wide);
         } else {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(b16 + cc * 32 + i) =
-                make_uint4(pack_bf16(ov[i], ov[i + 1]), pack_bf16(ov[i + 2], ov[i + 3]),
-                           pack_bf16(ov[i + 4], ov[i + 5]), pack_bf16(ov[i + 6], ov[i + 7]));
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(ov[2 * i], ov[2 * i + 1]);
+          store_row(b16 + cc * 32, w, wide);
         }
       }
       if (valid) {
@@ -769,8 +789,28 @@ __device__ __forceinline__ int32_t pair_tiles(int64_t cap, const Seq& s, int32_t
   return vis > 0 ? static_cast<int32_t>((vis + 127) >> 7) : 0;
 }
 
-constexpr int kCutUnits = 512;  // pairs that the cutting handles (two per SM is below)
+constexpr int kCutUnits = kPlanThreads;  // pairs that the cutting handles (two per SM is below)
 constexpr int kBuckets = 64;
+
+// What cutting costs, in the time of a key tile (1.6 us).  `big` items of about w
+// tiles set the rounds over the SMs, all of them the work to be spread; an item
+// costs kItemTiles besides its tiles (its first tile's chain, its result), and
+// partials a merge (54 of 128 KB in a tile's time, 4 to start).
+constexpr float kItemTiles = 4.f;
+__host__ __device__ inline float cut_cost(int64_t big, int64_t w, int64_t items, int64_t tiles,
+                                          int64_t partials, int sm_count) {
+  const float rounds = static_cast<float>((big + sm_count - 1) / sm_count) * (w + kItemTiles);
+  const float spread = (tiles + kItemTiles * items) / sm_count;
+  return (rounds > spread ? rounds : spread) + (partials > 0 ? 4.f + partials / 54.f : 0.f);
+}
+// Numbers of pieces that are tried: 1 to 16, then about a fifth more each time.
+constexpr int kCandidates = 32;
+__device__ __forceinline__ int candidate(int i) {
+  int k = i + 1;
+  if (k > 16)
+    for (k = 16; i > 15; --i) k += k / 5;
+  return k;
+}
 
 // One block: the units of all sequences, whether and how to cut them, and the
 // list of work, longest pieces first.  Latency-bound: about 4 us for a few
@@ -847,28 +887,32 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   __syncthreads();
   int32_t piece = longest > 0 ? longest : 1;
   if (may_cut && longest >= 2 * kMinPiece) {
-    // candidate k: the longest unit in k pieces.  Cost in key tiles: a CTA's
-    // rounds, each with a piece and an epilogue (1.5 tiles when it leaves
-    // partials), and the merge (54 pieces of 128 KB a tile's time, 3 to start)
-    const int k = t + 1;
-    const int32_t w = (longest + k - 1) / k;
-    unsigned long long mine_best = ~0ull;
-    if (k == 1 || w >= kMinPiece) {
-      int64_t n = 0;
-      for (int i = 0; i < n_pairs; ++i) n += tiles[i] > w ? (tiles[i] + w - 1) / w : 1;
-      if (k == 1 || n <= p.max_slots) {
-        const int64_t all = n * p.Hkv, rounds = (all + p.sm_count - 1) / p.sm_count;
-        // (as cut_cost; an uncut unit writes its result itself)
-        const float cost = rounds * (w + (k > 1 ? 1.5f : 0.f)) + (k > 1 ? 3.f + all / 54.f : 0.f);
-        mine_best = (static_cast<unsigned long long>(cost * 16.f) << 32) | static_cast<unsigned>(w);
-      }
-    }
+    // candidate k: the longest unit in k pieces, a warp each
+    int64_t all_tiles = 0;
+    for (int i = lane; i < n_pairs; i += 32) all_tiles += tiles[i];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const unsigned long long o = __shfl_xor_sync(0xffffffffu, mine_best, d);
-      mine_best = o < mine_best ? o : mine_best;
+    for (int d = 16; d > 0; d >>= 1) all_tiles += __shfl_xor_sync(0xffffffffu, all_tiles, d);
+    for (int c = t >> 5; c < kCandidates; c += kPlanThreads / 32) {
+      const int k = candidate(c);
+      const int32_t w = (longest + k - 1) / k;
+      if (k > 1 && w < kMinPiece) break;
+      int32_t n = 0, big = 0, slots = 0;  // pieces, those over half of w, those with partials
+      for (int i = lane; i < n_pairs; i += 32) {
+        const int32_t q = tiles[i] > w ? (tiles[i] + w - 1) / w : 1;
+        n += q;
+        if (2 * tiles[i] > w * q) big += q;
+        if (q > 1) slots += q;
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      big = __reduce_add_sync(0xffffffffu, big);
+      slots = __reduce_add_sync(0xffffffffu, slots);
+      if (k > 1 && slots > p.max_slots) continue;
+      const float cost = cut_cost(big * p.Hkv, w, n * p.Hkv, all_tiles * p.Hkv, slots * p.Hkv,
+                                  p.sm_count);
+      if (lane == 0)
+        atomicMin(&best, (static_cast<unsigned long long>(cost * 16.f) << 32) |
+                             static_cast<unsigned>(w));
     }
-    if (lane == 0 && mine_best != ~0ull) atomicMin(&best, mine_best);
     __syncthreads();
     piece = static_cast<int32_t>(best & 0xffffffffu);
   }
@@ -878,31 +922,35 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     size = (n + k - 1) / k;
     return size > 0 ? (n + size - 1) / size : 1;
   };
-  int32_t n_cut = 0, n_slots = 0;
-  if (may_cut && t < 32) {  // slots and list of the cut units
-    for (int base = 0; base < n_pairs; base += 32) {
-      const int i = base + lane;
-      int32_t size, k = i < n_pairs ? cut(tiles[i], size) : 0;
-      const int32_t need = k > 1 ? k : 0;
-      int32_t sum = need;
+  int32_t n_cut = 0;
+  if (may_cut) {  // slots and list of the cut units, unit t in thread t
+    int32_t size;
+    const int32_t k = t < n_pairs ? cut(tiles[t], size) : 0;
+    const int32_t need = k > 1 ? (1 << 16) + k : 0;  // (a unit, its slots)
+    int32_t sum = need;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    __syncthreads();  // (wsum was read above)
+    if (lane == 31) wsum[t >> 5] = sum;
+    __syncthreads();
+    int32_t all = 0, ahead = sum - need;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < (t >> 5)) ahead += static_cast<int32_t>(wsum[w]);
+      all += static_cast<int32_t>(wsum[w]);
+    }
+    n_cut = all >> 16;
+    if (t < n_pairs) {
+      slot0[t] = k > 1 ? ahead & 0xffff : -1;
+      if (k > 1) {
+        Seq s;
+        int32_t first;
+        unit(t, s, first);
+        p.cut[ahead >> 16] = CutUnit{
+            s.q0 + first, s.n - first < pair_tok ? s.n - first : pair_tok, ahead & 0xffff, k};
       }
-      const uint32_t cuts = __ballot_sync(0xffffffffu, k > 1);
-      if (i < n_pairs) {
-        slot0[i] = k > 1 ? n_slots + sum - need : -1;
-        if (k > 1) {
-          Seq s;
-          int32_t first;
-          unit(i, s, first);
-          p.cut[n_cut + __popc(cuts & ((1u << lane) - 1u))] =
-              CutUnit{s.q0 + first, s.n - first < pair_tok ? s.n - first : pair_tok, slot0[i], k};
-        }
-      }
-      n_slots += __shfl_sync(0xffffffffu, sum, 31);
-      n_cut += __popc(cuts);
     }
   }
   __syncthreads();
@@ -911,23 +959,35 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     const int32_t x = static_cast<int32_t>(static_cast<int64_t>(size) * (kBuckets - 1) / widest);
     return kBuckets - 1 - (x < kBuckets ? x : kBuckets - 1);
   };
+  // Every piece, piece-major, by whole warps: f(its bucket, -1 for none, the
+  // lanes of the warp with the same one, the piece as an entry).
   const int rounds = longest > piece ? (longest + piece - 1) / piece : 1;  // a unit's most pieces
-  auto each = [&](auto&& f) {  // piece-major
-    for (int64_t at = t; at < static_cast<int64_t>(rounds) * n_pairs; at += kPlanThreads) {
-      const int j = static_cast<int>(at / n_pairs), i = static_cast<int>(at % n_pairs);
-      Seq s;
-      int32_t first, size;
-      const int b = unit(i, s, first);
-      const int32_t nt = s.n - first < pair_tok ? s.n - first : pair_tok;
-      const int32_t n = pair_tiles(p.cap, s, first + nt - 1);
-      const int32_t k = cut(n, size);
-      if (j >= k) continue;
-      const int32_t left = n - j * size;
-      f(i, j, k, b, s, first, nt, left < size ? left : size, size);
+  auto each = [&](auto&& f) {
+    const int64_t count = static_cast<int64_t>(rounds) * n_pairs;
+    for (int64_t at = t; at - lane < count; at += kPlanThreads) {
+      int32_t key = -1;
+      Entry e{};
+      if (at < count) {
+        const int j = static_cast<int>(at / n_pairs), i = static_cast<int>(at % n_pairs);
+        Seq s;
+        int32_t first, size;
+        e.b = unit(i, s, first);
+        e.tok0 = s.q0 + first;
+        e.ntok = s.n - first < pair_tok ? s.n - first : pair_tok;
+        const int32_t n = pair_tiles(p.cap, s, first + e.ntok - 1);
+        const int32_t k = cut(n, size);
+        e.j0 = j * size;
+        e.size = n - e.j0 < size ? n - e.j0 : size;
+        e.len = static_cast<int32_t>(s.len > p.cap ? p.cap : s.len);
+        e.lim0 = s.len - s.n + first;
+        e.slot = k > 1 ? slot0[i] + j : -1;
+        if (j < k) key = bucket(e.size);
+      }
+      f(key, __match_any_sync(0xffffffffu, key), e);
     }
   };
-  each([&](int, int, int, int, const Seq&, int32_t, int32_t, int32_t now, int32_t) {
-    atomicAdd(&hist[bucket(now) + 1], 1);
+  each([&](int32_t key, uint32_t same, const Entry&) {
+    if (key >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[key + 1], __popc(same));
   });
   __syncthreads();
   if (t < 32) {
@@ -943,13 +1003,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   }
   __syncthreads();
   const int32_t total = hist[kBuckets];
-  each([&](int i, int j, int k, int b, const Seq& s, int32_t first, int32_t nt, int32_t now,
-           int32_t size) {
-    const int32_t at = atomicAdd(&hist[bucket(now)], 1);
-    const int64_t len = s.len > p.cap ? p.cap : s.len;
-    if (at < p.max_entries)
-      p.entries[at] = Entry{b, s.q0 + first, nt, j * size, now, static_cast<int32_t>(len),
-                            s.len - s.n + first, k > 1 ? slot0[i] + j : -1};
+  each([&](int32_t key, uint32_t same, const Entry& e) {
+    const int leader = __ffs(same) - 1;
+    int32_t at = 0;
+    if (key >= 0 && lane == leader) at = atomicAdd(&hist[key], __popc(same));
+    at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+    if (key >= 0 && at < p.max_entries) p.entries[at] = e;
   });
   if (t == 0) *p.header = Header{total < p.max_entries ? total : p.max_entries, n_cut};
 }
@@ -965,26 +1024,41 @@ struct FwdMergeParams {
   lsx_tensor o, lse;
 };
 
-// One warp per row of a cut unit.
+// One warp per two rows of a cut unit, both in flight together.
 template <int D>
-__global__ void __launch_bounds__(256, 3) paged_fwd_merge_kernel(const FwdMergeParams p) {
+__global__ void __launch_bounds__(256, 2) paged_fwd_merge_kernel(const FwdMergeParams p) {
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t rows = __ldcg(&p.header->n_cut) * p.Hkv * 256;
+  const int64_t pairs = __ldcg(&p.header->n_cut) * p.Hkv * 128;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < rows;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < pairs;
        i += step) {
-    const int row = static_cast<int>(i & 255);
-    const int64_t hk = (i >> 8) % p.Hkv;
-    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 8) / p.Hkv);
+    const int row = static_cast<int>(i & 127) * 2, t = row >> 7;
+    const int64_t hk = (i >> 7) % p.Hkv;
+    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 7) / p.Hkv);
     const CutUnit x{u.x, u.y, u.z, u.w};
-    const int r = row & 127, tok = r / p.G, t = row >> 7;
-    if (tok >= p.tpt || t * p.tpt + tok >= x.ntok) continue;
-    RowMerge<D> sum;
-    sum.take(p.part_o, p.part_l, x.n, lane, [&](int64_t c) {
-      return ((x.first + c) * p.Hkv + hk) * 256 + row;
-    });
-    sum.store(p.o, p.lse, 0, hk * p.G + (r - tok * p.G), x.tok0 + t * p.tpt + tok, lane);
+    int tok[2], head[2];
+    bool valid[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = (row & 127) + k;
+      tok[k] = r / p.G;
+      head[k] = r - tok[k] * p.G;
+      valid[k] = tok[k] < p.tpt && t * p.tpt + tok[k] < x.ntok;
+    }
+    if (!valid[0]) continue;  // (rows are in the order of the tokens)
+    auto row_of = [&](int64_t c) { return ((x.first + c) * p.Hkv + hk) * 256 + row; };
+    RowMerge<D> sum[2];
+    if (x.n <= 8) {
+      RowMerge<D>::take_two(sum, p.part_o, p.part_l, x.n, lane, row_of);
+    } else {
+      sum[0].take(p.part_o, p.part_l, x.n, lane, row_of);
+      sum[1].take(p.part_o, p.part_l, x.n, lane, [&](int64_t c) { return row_of(c) + 1; });
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (valid[k])
+        sum[k].store(p.o, p.lse, 0, hk * p.G + head[k], x.tok0 + t * p.tpt + tok[k], lane);
   }
 }
 
@@ -1048,8 +1122,7 @@ FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, i
   const int64_t tiles = ceil_div(max_pages * kp.N, 128);
   x.max_slots = tiles >= 2 * kMinPiece ? kPiecesPerSm * sm_count / kp.H : 0;
   if (x.max_slots < 2) x.max_slots = 0;
-  x.max_entries = ceil_div(q.N, 2 * tpt) + batch;
-  if (x.max_entries < x.max_slots) x.max_entries = x.max_slots;
+  x.max_entries = ceil_div(q.N, 2 * tpt) + batch + x.max_slots;
   x.entries = 256;
   x.cut = x.entries + align256(static_cast<size_t>(x.max_entries) * sizeof(Entry));
   x.part_l = x.cut + align256(kCutUnits * sizeof(CutUnit));
@@ -1057,15 +1130,6 @@ FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, i
   x.part_o = x.part_l + align256(rows * 4);
   x.total = x.part_o + align256(rows * static_cast<size_t>(q.D) * 4);
   return x;
-}
-
-// The cost, in the time of a key tile, of `units` units of `tiles` key tiles per
-// kv head cut into k pieces that leave partials: rounds over the SMs, each a piece and an
-// epilogue that writes 256 fp32 rows (1.5 tiles), and the merge, which reads
-// 54 such pieces of 128 KB in a tile's time.
-float cut_cost(int64_t units, int64_t tiles, int64_t k, int64_t hkv, int sm_count) {
-  const int64_t all = units * hkv * k;
-  return static_cast<float>(ceil_div(all, sm_count)) * (ceil_div(tiles, k) + 1.5f) + all / 54.f;
 }
 
 }  // namespace
@@ -1077,11 +1141,14 @@ PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, 
   x.tpt = static_cast<int>(128 / per);
   if (B < 2 * x.tpt) x.tpt = static_cast<int>(ceil_div(B, 2));
   const int64_t units = ceil_div(B, 2 * x.tpt), tiles = ceil_div(prefix_len, 128);
+  auto cost = [&](int64_t k) {
+    const int64_t n = units * hkv * k;
+    return cut_cost(n, ceil_div(tiles, k), n, units * hkv * tiles, n, sm_count);
+  };
   int64_t best = 1;
   for (int64_t k = 2; units * hkv * k <= kPiecesPerSm * sm_count && ceil_div(tiles, k) >= kMinPiece;
        ++k)
-    if (cut_cost(units, tiles, k, hkv, sm_count) < cut_cost(units, tiles, best, hkv, sm_count))
-      best = k;
+    if (cost(k) < cost(best)) best = k;
   x.size = static_cast<int>(ceil_div(tiles, best));
   x.pieces = static_cast<int>(ceil_div(tiles, x.size));
   x.rows = units * x.pieces * hkv * 256;
@@ -1107,6 +1174,7 @@ int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tens
   p.scale_log2 = scale * kLog2e;
   p.o = q;  // (not written: every row goes to the partials)
   p.lse = q;
+  p.wide = false;
   p.part_o = part_o;
   p.part_l = part_l;
   p.status = ctx.status;
@@ -1145,6 +1213,9 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   p.u_tokens = p.u_len = p.u_pieces = p.u_size = 0;
   p.scale_log2 = scale * kLog2e;
   p.o = o; p.lse = lse;
+  const int64_t unit = o.dtype == LSX_F32 ? 8 : 16;  // elements of 32 bytes
+  p.wide = reinterpret_cast<uintptr_t>(o.data) % 32 == 0 && o.stride_h % unit == 0 &&
+           o.stride_n % unit == 0;
   p.part_o = reinterpret_cast<float*>(ws + x.part_o);
   p.part_l = reinterpret_cast<float*>(ws + x.part_l);
   p.status = ctx.status;
