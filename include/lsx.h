@@ -357,7 +357,10 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  * masked), a length beyond the table counts as max_pages * page keys, a
  * negative length as 0; each but the last records LSX_ERR_PAGE in the status
  * word.  Rows of a page past a sequence's length are never used, whatever
- * they hold.  All calls are inference-only (no gradients).
+ * they hold.  The values before it have to be finite: an infinity or NaN there
+ * can reach queries that do not see it (a weight of 0 times it).  A score that
+ * is NaN or +infinity makes its query's O and LSE NaN.  All calls are
+ * inference-only (no gradients).
  *
  * attn_page_map -- one step's bookkeeping from the request lengths alone.
  *   ctx_lens, new_lens: int32 [batch] (1 <= batch <= 4096), the keys a
@@ -372,7 +375,8 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *     the first packed token of each sequence and their number; kv_lens int32
  *     [batch] = ctx + new; taken int32 [1], the pages asked for (more than
  *     n_free: the pool ran out).  The sums have to fit 31 bits.
- *   Calling it again with the same inputs gives the same results.
+ *   Calling it again with the same inputs gives the same results.  No output
+ *   may overlap ctx_lens, new_lens or free_pages (LSX_ERR_UNSUPPORTED).
  *
  * attn_page_append -- writes the new rows into their slots.
  *   k, v [1, Hkv, T, D] bf16, or f32 (each value rounded once); slot_map

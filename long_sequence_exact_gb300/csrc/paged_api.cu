@@ -59,6 +59,12 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return reinterpret_cast<uintptr_t>(ws) % 256 == 0 ? LSX_OK : LSX_ERR_ALIGN;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
+         y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 int sm_count_or(int fallback) {
   DeviceCtx ctx;
   return device_ctx(&ctx) == LSX_OK ? ctx.sm_count : fallback;
@@ -94,6 +100,14 @@ int attn_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batc
     if (slot_map == nullptr) return LSX_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(slot_map) % 8 != 0) return LSX_ERR_ALIGN;
   }
+  // thread blocks write results while others still read the inputs
+  const struct { const void* at; int64_t bytes; }
+      in[] = {{ctx_lens, 4 * batch}, {new_lens, 4 * batch}, {free_pages, 4 * n_free}},
+      out[] = {{block_table, 4 * ((batch - 1) * table_stride + max_pages)},
+               {slot_map, 8 * n_tokens}, {cu_new, 4 * (batch + 1)}, {kv_lens, 4 * batch}, {taken, 4}};
+  for (const auto& i : in)
+    for (const auto& o : out)
+      if (overlap(i.at, i.bytes, o.at, o.bytes)) return LSX_ERR_UNSUPPORTED;
   DeviceCtx ctx;
   LSX_TRY(device_ctx(&ctx));
   return launch_page_map(ctx_lens, new_lens, batch, free_pages, n_free, page_size, block_table,

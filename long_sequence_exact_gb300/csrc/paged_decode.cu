@@ -579,8 +579,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const int r = rt * 16 + qr + 8 * hh;
           int64_t b, h, n;
           if (!out_row(p, x.b, x.hk, r, b, h, n)) continue;
-          const float inv = l[hh] > 0.f ? 1.f / l[hh] : 0.f;
-          const float lse = l[hh] > 0.f ? (m[hh] + lg2(l[hh])) * kLn2 : kNegInf;
+          // (a row without keys has l = 0; a NaN score stays)
+          const float inv = l[hh] == 0.f ? 0.f : 1.f / l[hh];
+          const float lse = l[hh] == 0.f ? kNegInf : (m[hh] + lg2(l[hh])) * kLn2;
           if (direct) {
             const int64_t at = view_off(p.o, b, h, n) + qc;
             if (p.o.dtype == LSX_F32) {
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         s.x += po[c].x * w; s.y += po[c].y * w;
         s.z += po[c].z * w; s.w += po[c].w * w;
       }
-      const float inv = tot > 0.f ? 1.f / tot : 0.f;
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;
       int64_t b, h, n;
       if (out_row(p, x.b, x.hk, r, b, h, n)) {
         const int64_t at = view_off(p.o, b, h, n) + e;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
         if (e == 0)
           static_cast<float*>(p.lse.data)[view_off(p.lse, b, h, n)] =
-              tot > 0.f ? (mm + lg2(tot)) * kLn2 : kNegInf;
+              tot == 0.f ? kNegInf : (mm + lg2(tot)) * kLn2;
       }
     }
     cluster_sync();  // no CTA leaves while its rows are read

@@ -692,8 +692,9 @@ __global__ void __launch_bounds__(384, 1)
         if (!wait(&sm.o_full[t], s_phase ^ 1)) break;
         tc_fence_after();
       }
-      const float inv = (l > 0.f) ? 1.f / l : 0.f;
-      const float lse = (l > 0.f) ? (m + lg2(l)) * kLn2 : kNegInf;
+      // (a row without keys has l = 0; a NaN score stays)
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse = l == 0.f ? kNegInf : (m + lg2(l)) * kLn2;
       const bool part = x.e.slot >= 0;
       const int64_t prow =
           (static_cast<int64_t>(x.e.slot) * p.Hkv + x.hk) * 256 + t * 128 + row;
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(384, 1)
         if (!valid) continue;
         float ov[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) ov[i] = l > 0.f ? __uint_as_float(u[i]) * inv : 0.f;
+        for (int i = 0; i < 32; ++i) ov[i] = l == 0.f ? 0.f : __uint_as_float(u[i]) * inv;
         if (f32 != nullptr) {
           uint32_t w[32];
 #pragma unroll

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -42,7 +43,7 @@ struct RowMerge {
       };
       load(0);  // (in flight while the weights are formed)
       const float mine = lane < n ? __ldcg(l + row_of(c0 + lane)) : kNone;
-      float mx = mine;
+      float mx = isnan(mine) ? -kNone : mine;  // (NaN weights, and so a NaN row)
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
       const float m_new = fmaxf(m, mx);
@@ -95,7 +96,7 @@ struct RowMerge {
       }
     const int part = lane & 7;
     const float mine = lane < 16 && part < count ? __ldcg(l + row_of(part) + (lane >> 3)) : kNone;
-    float mx = mine;
+    float mx = isnan(mine) ? -kNone : mine;
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     const float w = mine == kNone ? 0.f : ex2((mine - mx) * kLog2);
@@ -119,7 +120,7 @@ struct RowMerge {
   // The row (b, h, n) of o and lse.
   __device__ __forceinline__ void store(const lsx_tensor& o, const lsx_tensor& lse, int64_t b,
                                         int64_t h, int64_t n, int lane) const {
-    const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
     const int64_t at = view_off(o, b, h, n) + lane * E;
     if (o.dtype == LSX_F32) {
 #pragma unroll
@@ -132,7 +133,7 @@ struct RowMerge {
     }
     if (lane == 0)
       static_cast<float*>(lse.data)[view_off(lse, b, h, n)] =
-          tot > 0.f ? m + lg2(tot) * 0.6931471805599453f : -__builtin_huge_valf();
+          tot == 0.f ? -__builtin_huge_valf() : m + lg2(tot) * 0.6931471805599453f;
   }
 };
 

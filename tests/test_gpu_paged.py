@@ -387,6 +387,80 @@ def test_paged_fwd_random(i):
     check_prompt(out, lse, o_ref, l_ref, tol, tol_lse)
 
 
+@pytest.mark.parametrize("case", [
+    (1, 1, 128, 16, [(9000, 3)]),                             # one unit in more than eight pieces
+    (2, 1, 64, 32, [(2500, 130), (0, 0), (1200, 5)]),         # cut and whole units
+    (3, 3, 128, 64, [(1100 * (i % 2), 2) for i in range(20)]),
+    (1, 1, 64, 16, [(i % 7, i % 2) for i in range(1100)]),    # more units than are cut, and empty ones
+    (1, 1, 64, 16, [(1500, 1) if i % 200 == 7 else (5, 0) for i in range(1000)]),
+], ids=["nine", "mixed", "heads", "many", "few"])
+def test_paged_fwd_cut_units(case):
+    """Long keys over few tokens: pieces and their merge; with outputs that are
+    aligned to 16 bytes only."""
+    q, kp, vp, table, lens, cu = prompt_case(*case, tail=2)
+    o_ref, l_ref = P.fwd(q, kp, vp, table, lens, cu)
+    bounds = {t: P.tolerances(q, kp, vp, P_BF16, t) for t in (torch.float32, torch.bfloat16)}
+    poison(kp, vp, table, lens, case[3])
+    lse = torch.full(q.shape[:3], 7.0, device=DEV)
+    for dtype, shift in ((torch.float32, 0), (torch.float32, 4), (torch.bfloat16, 0), (torch.bfloat16, 8)):
+        tol, tol_lse = bounds[dtype]
+        flat = torch.full((q.numel() + 8,), 7.0, dtype=dtype, device=DEV)
+        out = flat[shift:shift + q.numel()].view(q.shape)
+        assert out.data_ptr() % 32 == (16 if shift else 0)
+        lsx.paged_fwd(q, kp, vp, table, ints(lens), ints(cu), out=out, lse=lse)
+        assert done() == 0
+        check_prompt(out, lse, o_ref, l_ref, tol, tol_lse)
+
+
+def check_nan_rows(o, lse, o_ref, l_ref, sees, tol, tol_lse):
+    """NaN in the rows that see the NaN score, the reference elsewhere."""
+    o, lse = f64(o), f64(lse)
+    assert np.isnan(lse[sees]).all() and np.isnan(o[sees]).all()
+    check_lse(lse[~sees], l_ref[~sees], tol_lse)
+    check_close(o[~sees], o_ref[~sees], tol)
+
+
+@pytest.mark.parametrize("seq", [(100, 300), (3000, 40)])  # whole; cut into pieces
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_fwd_nan_scores(seq, d):
+    q, kp, vp, table, lens, cu = prompt_case(4, 2, d, 16, [seq, (0, 50)])
+    tol, tol_lse = P.tolerances(q, kp, vp, P_BF16, torch.float32)
+    o_ref, l_ref = P.fwd(q, kp, vp, table, lens, cu)
+    at, bad = seq[0] + 20, seq[1] + 7                 # a key of the first sequence, a token of the second
+    kp[int(table[0, at // 16]), 0, at % 16, 3] = float("nan")
+    q[0, 3, bad] = float("nan")
+    sees = np.zeros(l_ref.shape, bool)
+    sees[0, :2, 20:seq[1]] = True
+    sees[0, 3, bad] = True
+    o, lse = lsx.paged_fwd(q, kp, vp, table, ints(lens), ints(cu), out_dtype=torch.float32)
+    assert done() == 0
+    check_nan_rows(o, lse, o_ref, l_ref, sees, tol, tol_lse)
+
+
+@pytest.mark.parametrize("lens,prefix_len,keys", [
+    ([700, 40], 0, 0),                 # a cluster each
+    ([700, 40], 0, 40000),             # runs
+    ([9000, 40], 0, 40000),            # a unit in many runs
+    ([700, 40], 300, 0),               # behind a prefix, few rows
+    ([700, 40] + [5] * 20, 300, 0),    # behind a prefix, many
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_decode_nan_scores(lens, prefix_len, keys, d):
+    q, kp, vp, table, prefix = decode_case(4, 2, 2, d, 16, lens, prefix_len, width=keys // 16)
+    tol, tol_lse = P.tolerances(q, kp, vp, p_rounding(q, kp, prefix_len), torch.float32)
+    o_ref, l_ref = P.decode(q, kp, vp, table, lens, prefix, prefix_len)
+    at = lens[0] - 1                                  # the last key: of the last query token alone
+    kp[int(table[0, at // 16]), 0, at % 16, 3] = float("nan")
+    q[1, 3, 0] = float("nan")
+    sees = np.zeros(l_ref.shape, bool)
+    sees[0, :2, 1] = True
+    sees[1, 3, 0] = True
+    o, lse = lsx.paged_decode(q, kp, vp, table, ints(lens), prefix_table=ints(prefix) if prefix_len else None,
+                              prefix_len=prefix_len, out_dtype=torch.float32)
+    assert done() == 0
+    check_nan_rows(o, lse, o_ref, l_ref, sees, tol, tol_lse)
+
+
 def test_paged_fwd_leaves_out_pages_that_do_not_exist():
     q, kp, vp, table, lens, cu = prompt_case(4, 2, 128, 16, [(100, 60), (0, 33), (0, 16)])
     table[0, 1], table[0, 7], table[1, 1] = -1, kp.shape[0], 2 ** 31 - 1

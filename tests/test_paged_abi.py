@@ -144,6 +144,12 @@ def test_map_refusals(lib):
     assert map_(lib, stride=4) == SHAPE
     for page in (0, 8, 48, 512):
         assert map_(lib, page=page) == UNSUP
+    # outputs over inputs: blocks that still read them would see what others wrote
+    assert map_(lib, lens=0x1000) == UNSUP                     # lengths updated in place
+    assert map_(lib, cu=0x1104) == UNSUP
+    assert map_(lib, taken=0x1220) == UNSUP                    # the last free page
+    assert map_(lib, slots=0x11e0) == UNSUP                    # runs into the free pages
+    assert map_(lib, table=0xfc8) == UNSUP                     # 15 entries: one in the lengths
 
 
 def append(lib, k=None, v=None, slots=0x5000, kp=None, vp=None):
