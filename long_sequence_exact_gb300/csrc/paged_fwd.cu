@@ -798,24 +798,22 @@ constexpr int kBuckets = 64;
 // costs kItemTiles besides its tiles (its first tile's chain, its result), and
 // partials a merge (54 of 128 KB in a tile's time, 4 to start).
 constexpr float kItemTiles = 4.f;
-__host__ __device__ inline float cut_cost(int64_t big, int64_t w, int64_t items, int64_t tiles,
-                                          int64_t partials, int sm_count) {
-  const float rounds = static_cast<float>((big + sm_count - 1) / sm_count) * (w + kItemTiles);
-  const float spread = (tiles + kItemTiles * items) / sm_count;
-  return (rounds > spread ? rounds : spread) + (partials > 0 ? 4.f + partials / 54.f : 0.f);
+__host__ __device__ inline float cut_cost(float big, float w, float items, float tiles,
+                                          float partials, int sm_count) {
+  const float each = 1.f / sm_count;
+  const float rounds = ceilf((big - 0.5f) * each) * (w + kItemTiles);
+  const float spread = (tiles + kItemTiles * items) * each;
+  return (rounds > spread ? rounds : spread) + (partials > 0 ? 4.f + partials * (1.f / 54.f) : 0.f);
 }
 // Numbers of pieces that are tried: 1 to 16, then about a fifth more each time.
 constexpr int kCandidates = 32;
 __device__ __forceinline__ int candidate(int i) {
-  int k = i + 1;
-  if (k > 16)
-    for (k = 16; i > 15; --i) k += k / 5;
-  return k;
+  return i < 16 ? i + 1 : static_cast<int>(16.f * ex2(0.263034406f * (i - 15)));
 }
 
 // One block: the units of all sequences, whether and how to cut them, and the
-// list of work, longest pieces first.  Latency-bound: about 4 us for a few
-// sequences; the next launch's set-up runs meanwhile.
+// list of work, longest pieces first.  Latency-bound: 5 to 7 us; the next
+// launch's set-up runs meanwhile.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int32_t start[];  // [batch + 1] first pair of each sequence
   Seq* const seqs = reinterpret_cast<Seq*>(start + p.batch + 1);
@@ -908,8 +906,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
       big = __reduce_add_sync(0xffffffffu, big);
       slots = __reduce_add_sync(0xffffffffu, slots);
       if (k > 1 && slots > p.max_slots) continue;
-      const float cost = cut_cost(big * p.Hkv, w, n * p.Hkv, all_tiles * p.Hkv, slots * p.Hkv,
-                                  p.sm_count);
+      const float h = p.Hkv, cost = cut_cost(big * h, w, n * h, all_tiles * h, slots * h, p.sm_count);
       if (lane == 0)
         atomicMin(&best, (static_cast<unsigned long long>(cost * 16.f) << 32) |
                              static_cast<unsigned>(w));
@@ -957,19 +954,19 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   __syncthreads();
   const int32_t widest = piece > 0 ? piece : 1;
   auto bucket = [&](int32_t size) {  // 0: the longest
-    const int32_t x = static_cast<int32_t>(static_cast<int64_t>(size) * (kBuckets - 1) / widest);
+    const int32_t x = size * (kBuckets - 1) / widest;  // (fewer than 2^24 tiles)
     return kBuckets - 1 - (x < kBuckets ? x : kBuckets - 1);
   };
   // Every piece, piece-major, by whole warps: f(its bucket, -1 for none, the
   // lanes of the warp with the same one, the piece as an entry).
   const int rounds = longest > piece ? (longest + piece - 1) / piece : 1;  // a unit's most pieces
   auto each = [&](auto&& f) {
-    const int64_t count = static_cast<int64_t>(rounds) * n_pairs;
-    for (int64_t at = t; at - lane < count; at += kPlanThreads) {
+    const int32_t count = rounds * n_pairs;  // (rounds > 1: few pairs, few pieces)
+    for (int32_t at = t; at - lane < count; at += kPlanThreads) {
       int32_t key = -1;
       Entry e{};
       if (at < count) {
-        const int j = static_cast<int>(at / n_pairs), i = static_cast<int>(at % n_pairs);
+        const int j = at / n_pairs, i = at - j * n_pairs;
         Seq s;
         int32_t first, size;
         e.b = unit(i, s, first);
@@ -1025,19 +1022,23 @@ struct FwdMergeParams {
   lsx_tensor o, lse;
 };
 
-// One warp per two rows of a cut unit, both in flight together.
+// A warp takes two rows of a cut unit, all their pieces in flight together, or one
+// row where there are more than eight pieces (18 pieces 12.3 us by twos, 9.8 us).
 template <int D>
 __global__ void __launch_bounds__(256, 2) paged_fwd_merge_kernel(const FwdMergeParams p) {
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t pairs = __ldcg(&p.header->n_cut) * p.Hkv * 128;
+  const int64_t rows = __ldcg(&p.header->n_cut) * p.Hkv * 256;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < pairs;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < rows;
        i += step) {
-    const int row = static_cast<int>(i & 127) * 2, t = row >> 7;
-    const int64_t hk = (i >> 7) % p.Hkv;
-    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 7) / p.Hkv);
+    // (the low bit last: the rows that two-row warps leave out come behind the others)
+    const int at = static_cast<int>(i & 255), row = (at & 127) * 2 + (at >> 7), t = row >> 7;
+    const int64_t hk = (i >> 8) % p.Hkv;
+    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 8) / p.Hkv);
     const CutUnit x{u.x, u.y, u.z, u.w};
+    const bool two = x.n <= 8;
+    if (two && (row & 1) != 0) continue;
     int tok[2], head[2];
     bool valid[2];
 #pragma unroll
@@ -1045,17 +1046,15 @@ __global__ void __launch_bounds__(256, 2) paged_fwd_merge_kernel(const FwdMergeP
       const int r = (row & 127) + k;
       tok[k] = r / p.G;
       head[k] = r - tok[k] * p.G;
-      valid[k] = tok[k] < p.tpt && t * p.tpt + tok[k] < x.ntok;
+      valid[k] = (k == 0 || two) && tok[k] < p.tpt && t * p.tpt + tok[k] < x.ntok;
     }
     if (!valid[0]) continue;  // (rows are in the order of the tokens)
     auto row_of = [&](int64_t c) { return ((x.first + c) * p.Hkv + hk) * 256 + row; };
     RowMerge<D> sum[2];
-    if (x.n <= 8) {
+    if (two)
       RowMerge<D>::take_two(sum, p.part_o, p.part_l, x.n, lane, row_of);
-    } else {
+    else
       sum[0].take(p.part_o, p.part_l, x.n, lane, row_of);
-      sum[1].take(p.part_o, p.part_l, x.n, lane, [&](int64_t c) { return row_of(c) + 1; });
-    }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (valid[k])
@@ -1257,7 +1256,7 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   if (rc != LSX_OK || x.max_slots == 0) return rc;
   const FwdMergeParams mp{pp.header, pp.cut, p.Hkv, p.G, p.tpt, p.part_o, p.part_l, o, lse};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(4 * ctx.sm_count));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * ctx.sm_count));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
