@@ -6,9 +6,9 @@
 //
 // Bound: the tensor cores (4 D operations per visible (query, key) pair), for
 // few tokens the cache's bytes.  32 query and 8 kv heads of 128: 12345 tokens
-// 0.776 ms, 1.61 PFLOP/s; 32768 tokens 5.54 ms, 1.59 PFLOP/s; 512 tokens after 65536
-// keys 0.390 ms, of which the partials' merge 0.015; heads of 64, 32768 tokens
-// 4.35 ms, 1.01 PFLOP/s.
+// 0.772 ms, 1.62 PFLOP/s; 32768 tokens 5.50 ms, 1.60 PFLOP/s; 512 tokens after 65536
+// keys 0.380 ms, of which the partials' merge 0.011; heads of 64, 32768 tokens
+// 4.46 ms, 0.99 PFLOP/s.
 //
 // Rows.  The heads that share a key head are rows of one tile: row r of a
 // 128-row query tile is head r % G of token r / G, floor(128 / G) tokens a tile,
@@ -1022,43 +1022,27 @@ struct FwdMergeParams {
   lsx_tensor o, lse;
 };
 
-// A warp takes two rows of a cut unit, all their pieces in flight together, or one
-// row where there are more than eight pieces (18 pieces 12.3 us by twos, 9.8 us).
+// One warp per row of a cut unit, three blocks an SM (448 pieces of 128 KB 16.0 us
+// with the events around the launch, at two blocks 19.0; four blocks take 1.8 us
+// more for few rows).
 template <int D>
-__global__ void __launch_bounds__(256, 2) paged_fwd_merge_kernel(const FwdMergeParams p) {
+__global__ void __launch_bounds__(256, 3) paged_fwd_merge_kernel(const FwdMergeParams p) {
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t rows = __ldcg(&p.header->n_cut) * p.Hkv * 256;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < rows;
        i += step) {
-    // (the low bit last: the rows that two-row warps leave out come behind the others)
-    const int at = static_cast<int>(i & 255), row = (at & 127) * 2 + (at >> 7), t = row >> 7;
+    const int row = static_cast<int>(i & 255), t = row >> 7;
     const int64_t hk = (i >> 8) % p.Hkv;
     const int4 u = __ldcg(reinterpret_cast<const int4*>(p.cut) + (i >> 8) / p.Hkv);
     const CutUnit x{u.x, u.y, u.z, u.w};
-    const bool two = x.n <= 8;
-    if (two && (row & 1) != 0) continue;
-    int tok[2], head[2];
-    bool valid[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = (row & 127) + k;
-      tok[k] = r / p.G;
-      head[k] = r - tok[k] * p.G;
-      valid[k] = (k == 0 || two) && tok[k] < p.tpt && t * p.tpt + tok[k] < x.ntok;
-    }
-    if (!valid[0]) continue;  // (rows are in the order of the tokens)
-    auto row_of = [&](int64_t c) { return ((x.first + c) * p.Hkv + hk) * 256 + row; };
-    RowMerge<D> sum[2];
-    if (two)
-      RowMerge<D>::take_two(sum, p.part_o, p.part_l, x.n, lane, row_of);
-    else
-      sum[0].take(p.part_o, p.part_l, x.n, lane, row_of);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (valid[k])
-        sum[k].store(p.o, p.lse, 0, hk * p.G + head[k], x.tok0 + t * p.tpt + tok[k], lane);
+    const int tok = (row & 127) / p.G;
+    if (tok >= p.tpt || t * p.tpt + tok >= x.ntok) continue;
+    RowMerge<D> sum;
+    sum.take(p.part_o, p.part_l, x.n, lane,
+             [&](int64_t c) { return ((x.first + c) * p.Hkv + hk) * 256 + row; });
+    sum.store(p.o, p.lse, 0, hk * p.G + (row & 127) - tok * p.G, x.tok0 + t * p.tpt + tok, lane);
   }
 }
 
@@ -1256,7 +1240,7 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   if (rc != LSX_OK || x.max_slots == 0) return rc;
   const FwdMergeParams mp{pp.header, pp.cut, p.Hkv, p.G, p.tpt, p.part_o, p.part_l, o, lse};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * ctx.sm_count));
+  cfg.gridDim = dim3(static_cast<unsigned>(3 * ctx.sm_count));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr{};

@@ -70,53 +70,6 @@ struct RowMerge {
     }
   }
 
-  // Two neighbouring rows (row_of(i) and the next) with at most eight partials
-  // each, all loads in flight together: lanes 0..7 hold the first row's weights,
-  // lanes 8..15 the second's.
-  template <class F>
-  static __device__ __forceinline__ void take_two(RowMerge (&s)[2], const float* o, const float* l,
-                                                  int count, int lane, F&& row_of) {
-    constexpr float kNone = -__builtin_huge_valf();
-    constexpr float kLog2 = 1.4426950408889634f;
-    float y[2][8][E];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < count) {
-        const float* src = o + row_of(i) * D + lane * E;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if constexpr (E == 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + k * D));
-            y[k][i][0] = f.x; y[k][i][1] = f.y; y[k][i][2] = f.z; y[k][i][3] = f.w;
-          } else {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(src + k * D));
-            y[k][i][0] = f.x; y[k][i][1] = f.y;
-          }
-        }
-      }
-    const int part = lane & 7;
-    const float mine = lane < 16 && part < count ? __ldcg(l + row_of(part) + (lane >> 3)) : kNone;
-    float mx = isnan(mine) ? -kNone : mine;
-#pragma unroll
-    for (int d = 4; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float w = mine == kNone ? 0.f : ex2((mine - mx) * kLog2);
-    float sum = w;
-#pragma unroll
-    for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      s[k].m = __shfl_sync(0xffffffffu, mx, 8 * k);
-      s[k].tot = __shfl_sync(0xffffffffu, sum, 8 * k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, 8 * k + i);
-        if (i < count && s[k].m != kNone)
-#pragma unroll
-          for (int e = 0; e < E; ++e) s[k].acc[e] = fmaf(wi, y[k][i][e], s[k].acc[e]);
-      }
-    }
-  }
-
   // The row (b, h, n) of o and lse.
   __device__ __forceinline__ void store(const lsx_tensor& o, const lsx_tensor& lse, int64_t b,
                                         int64_t h, int64_t n, int lane) const {
