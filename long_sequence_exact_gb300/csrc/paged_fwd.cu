@@ -8,7 +8,7 @@
 // few tokens the cache's bytes.  32 query and 8 kv heads of 128: 12345 tokens
 // 0.772 ms, 1.62 PFLOP/s; 32768 tokens 5.50 ms, 1.60 PFLOP/s; 512 tokens after 65536
 // keys 0.380 ms, of which the partials' merge 0.011; heads of 64, 32768 tokens
-// 4.46 ms, 0.99 PFLOP/s.
+// 4.36 ms, 1.01 PFLOP/s.
 //
 // Rows.  The heads that share a key head are rows of one tile: row r of a
 // 128-row query tile is head r % G of token r / G, floor(128 / G) tokens a tile,
@@ -51,7 +51,11 @@
 // Measured and not kept: P published in halves (a wait more: +7%, and nothing
 // once the rest was short), O's barrier once per item (+2%), scores read from
 // TMEM in parts between the exponentials (+7% to +14%), the next tile prefetched
-// into L2 (+1% to +50%; -3% where a prefix streams from HBM).
+// into L2 (+1% to +50%; -3% where a prefix streams from HBM), an issuing thread per
+// query tile (+28%, heads of 64 +22%: the tiles' products interleave, and each
+// waits for both), for heads of 64 the next scores beside the weights, in TMEM
+// that heads of 128 do not have left (-1% ahead of the tile's product, +8% as soon
+// as the scores before are read).
 //
 // Pages.  A tile of 128 keys is 128 / page boxes of a page each (one for pages
 // of 128 and more).  A page past the length or one that does not exist is
@@ -623,17 +627,17 @@ __global__ void __launch_bounds__(384, 1)
           const float2 nm2 = make_float2(-m, -m);
           float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t pk[16];
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t pk[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 32; ++i) {
               const float2 arg =
-                  __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
+                  __ffma2_rn(make_float2(s[cc * 64 + 2 * i], s[cc * 64 + 2 * i + 1]), sc2, nm2);
               const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
               if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
               pk[i] = pack_bf16(e.x, e.y);
             }
-            tmem_st16(tS + cc * 16, pk);
+            tmem_st32(tS + cc * 32, pk);
           }
           return (la.x + la.y) + (lb.x + lb.y);
         };
