@@ -1130,13 +1130,17 @@ PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, 
   if (B < 2 * x.tpt) x.tpt = static_cast<int>(ceil_div(B, 2));
   const int64_t units = ceil_div(B, 2 * x.tpt), tiles = ceil_div(prefix_len, 128);
   auto cost = [&](int64_t k) {
-    const int64_t n = units * hkv * k;
-    return cut_cost(n, ceil_div(tiles, k), n, units * hkv * tiles, n, sm_count);
+    const float n = static_cast<float>(units * hkv * k);
+    return cut_cost(n, static_cast<float>(ceil_div(tiles, k)), n,
+                    static_cast<float>(units * hkv * tiles), n, sm_count);
   };
   int64_t best = 1;
+  float least = cost(1);
   for (int64_t k = 2; units * hkv * k <= kPiecesPerSm * sm_count && ceil_div(tiles, k) >= kMinPiece;
-       ++k)
-    if (cost(k) < cost(best)) best = k;
+       ++k) {
+    const float c = cost(k);
+    if (c < least) { best = k; least = c; }
+  }
   x.size = static_cast<int>(ceil_div(tiles, best));
   x.pieces = static_cast<int>(ceil_div(tiles, x.size));
   x.rows = units * x.pieces * hkv * 256;
