@@ -401,7 +401,8 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *   tokens sees keys j <= kv_len - n + i.  Hq / Hkv <= 128.  o, lse as q; rows
  *   that belong to no sequence are left as they were.  P is rounded to bf16.
  *
- * Both need the workspace their *_workspace_size names (256-byte aligned).
+ * Both need the workspace their *_workspace_size names (256-byte aligned); 0 where
+ * the sizes are refused, which the call then says.
  * ---------------------------------------------------------------------- */
 int attn_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch,
                   const int32_t* free_pages, int64_t n_free, int64_t page_size,

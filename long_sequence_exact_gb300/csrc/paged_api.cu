@@ -6,33 +6,71 @@
 namespace lsx {
 namespace {
 
-// pages [P, Hkv, page, D] for keys and values, bf16, the same shape.
+// The checks of sizes alone, which the calls share with their workspace sizes
+// (those are asked for before a call is checked, with any numbers).
+
+// pages [P, Hkv, page, D]
+int check_page_sizes(const lsx_tensor& kp) {
+  if (kp.B <= 0 || kp.H <= 0 || kp.N < 0 || kp.D <= 0) return LSX_ERR_SHAPE;
+  if (kp.D != 64 && kp.D != 128) return LSX_ERR_UNSUPPORTED;
+  if (kp.N < kMinPage || kp.N > kMaxPage || (kp.N & (kp.N - 1)) != 0) return LSX_ERR_UNSUPPORTED;
+  if (kp.B >= (int64_t{1} << 31) || kp.H >= (1 << 16)) return LSX_ERR_UNSUPPORTED;
+  return LSX_OK;
+}
+
+// q [B, Hq, N, D], the query heads a multiple of the cache's.
+int check_query_sizes(const lsx_tensor& q, const lsx_tensor& kp) {
+  if (q.B <= 0 || q.H <= 0 || q.N < 0) return LSX_ERR_SHAPE;
+  if (q.D != kp.D || q.H % kp.H != 0) return LSX_ERR_SHAPE;
+  const int64_t lim = int64_t{1} << 31;
+  if (q.N >= lim || q.H >= (1 << 16) || q.B >= (1 << 16)) return LSX_ERR_UNSUPPORTED;
+  return LSX_OK;
+}
+
+// What a table row can hold: positions, rounded up to a tile, are 32-bit.
+int check_table_size(int64_t max_pages, int64_t page) {
+  if (max_pages < 0) return LSX_ERR_SHAPE;
+  if (max_pages >= (int64_t{1} << 31) || max_pages * page > (int64_t{1} << 31) - 2 * kMaxPage)
+    return LSX_ERR_UNSUPPORTED;
+  return LSX_OK;
+}
+
+int check_decode_rows(const lsx_tensor& q, const lsx_tensor& kp) {
+  if (q.N < 1) return LSX_ERR_SHAPE;
+  return q.H / kp.H * q.N > kMaxDecodeRows ? LSX_ERR_UNSUPPORTED : LSX_OK;
+}
+
+int check_prefix_size(int64_t prefix_len) {
+  if (prefix_len < 0) return LSX_ERR_SHAPE;
+  return prefix_len > (int64_t{1} << 31) - 2 * kMaxPage ? LSX_ERR_UNSUPPORTED : LSX_OK;
+}
+
+int check_prompt_sizes(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch) {
+  if (q.B != 1 || batch <= 0) return LSX_ERR_SHAPE;
+  return batch > kMaxMapBatch || q.H / kp.H > 128 ? LSX_ERR_UNSUPPORTED : LSX_OK;
+}
+
+// keys and values in pages, bf16, the same shape.
 int check_pages(const lsx_tensor* kp, const lsx_tensor* vp) {
   LSX_TRY(check_view(kp));
   LSX_TRY(check_view(vp));
   if (kp->data == nullptr || vp->data == nullptr) return LSX_ERR_NULL;
   if (kp->dtype != LSX_BF16 || vp->dtype != LSX_BF16) return LSX_ERR_DTYPE;
   if (!same_bhn_d(kp, vp)) return LSX_ERR_SHAPE;
-  if (kp->D != 64 && kp->D != 128) return LSX_ERR_UNSUPPORTED;
-  if (kp->N < kMinPage || kp->N > kMaxPage || (kp->N & (kp->N - 1)) != 0)
-    return LSX_ERR_UNSUPPORTED;
-  if (kp->B >= (int64_t{1} << 31) || kp->H >= (1 << 16)) return LSX_ERR_UNSUPPORTED;
+  LSX_TRY(check_page_sizes(*kp));
   LSX_TRY(check_row_aligned(kp));
   LSX_TRY(check_row_aligned(vp));
   return LSX_OK;
 }
 
-// q, o [B, Hq, N, D] (q bf16, o bf16 or f32), lse [B, Hq, N, 1], and the
-// query heads a multiple of the cache's.
+// q, o [B, Hq, N, D] (q bf16, o bf16 or f32), lse [B, Hq, N, 1].
 int check_queries(const lsx_tensor* q, const lsx_tensor* kp, const lsx_tensor* o,
                   const lsx_tensor* lse) {
   LSX_TRY(check_view(q));
   LSX_TRY(check_view(o));
   if (q->dtype != LSX_BF16) return LSX_ERR_DTYPE;
-  if (q->D != kp->D || !same_bhn_d(q, o)) return LSX_ERR_SHAPE;
-  if (q->H % kp->H != 0) return LSX_ERR_SHAPE;
-  const int64_t lim = int64_t{1} << 31;
-  if (q->N >= lim || q->H >= (1 << 16) || q->B >= (1 << 16)) return LSX_ERR_UNSUPPORTED;
+  if (!same_bhn_d(q, o)) return LSX_ERR_SHAPE;
+  LSX_TRY(check_query_sizes(*q, *kp));
   LSX_TRY(check_row_aligned(q));
   LSX_TRY(check_row_aligned(o));
   if (q->N == 0) return LSX_OK;
@@ -46,10 +84,8 @@ int check_ints(const void* p) {
 
 // block table [batch][max_pages], rows table_stride apart
 int check_table(const int32_t* table, int64_t table_stride, int64_t max_pages, int64_t page) {
-  if (max_pages < 0 || table_stride < max_pages) return LSX_ERR_SHAPE;
-  // positions, rounded up to a tile, are 32-bit
-  if (max_pages >= (int64_t{1} << 31) || max_pages * page > (int64_t{1} << 31) - 2 * kMaxPage)
-    return LSX_ERR_UNSUPPORTED;
+  if (table_stride < max_pages) return LSX_ERR_SHAPE;
+  LSX_TRY(check_table_size(max_pages, page));
   return max_pages == 0 ? LSX_OK : check_ints(table);
 }
 
@@ -136,7 +172,10 @@ int attn_page_append(const lsx_tensor* k, const lsx_tensor* v, const int64_t* sl
 
 size_t attn_paged_decode_workspace_size(const lsx_tensor* q, const lsx_tensor* k_pages,
                                         int64_t max_pages, int64_t prefix_len) {
-  if (q == nullptr || k_pages == nullptr || k_pages->H <= 0 || q->H % k_pages->H != 0) return 0;
+  if (q == nullptr || k_pages == nullptr || check_page_sizes(*k_pages) != LSX_OK ||
+      check_query_sizes(*q, *k_pages) != LSX_OK || check_decode_rows(*q, *k_pages) != LSX_OK ||
+      check_table_size(max_pages, k_pages->N) != LSX_OK || check_prefix_size(prefix_len) != LSX_OK)
+    return 0;  // the call itself is refused, and says why
   return paged_decode_workspace(*q, *k_pages, max_pages, prefix_len, sm_count_or(kSmFallback));
 }
 
@@ -147,12 +186,10 @@ int attn_paged_decode(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_
                       size_t workspace_bytes, lsx_stream_t stream) {
   LSX_TRY(check_pages(k_pages, v_pages));
   LSX_TRY(check_queries(q, k_pages, o, lse));
-  if (q->N < 1) return LSX_ERR_SHAPE;
-  if (q->H / k_pages->H * q->N > kMaxDecodeRows) return LSX_ERR_UNSUPPORTED;
+  LSX_TRY(check_decode_rows(*q, *k_pages));
   LSX_TRY(check_table(block_table, table_stride, max_pages, k_pages->N));
   LSX_TRY(check_ints(kv_lens));
-  if (prefix_len < 0) return LSX_ERR_SHAPE;
-  if (prefix_len > (int64_t{1} << 31) - 2 * kMaxPage) return LSX_ERR_UNSUPPORTED;
+  LSX_TRY(check_prefix_size(prefix_len));
   if (prefix_len > 0) LSX_TRY(check_ints(prefix_table));
   LSX_TRY(check_ws(workspace, workspace_bytes,
                    attn_paged_decode_workspace_size(q, k_pages, max_pages, prefix_len)));
@@ -166,7 +203,11 @@ int attn_paged_decode(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_
 
 size_t attn_paged_fwd_workspace_size(const lsx_tensor* q, const lsx_tensor* k_pages,
                                      int64_t batch, int64_t max_pages) {
-  if (q == nullptr || k_pages == nullptr || k_pages->H <= 0 || q->H % k_pages->H != 0) return 0;
+  if (q == nullptr || k_pages == nullptr || check_page_sizes(*k_pages) != LSX_OK ||
+      check_query_sizes(*q, *k_pages) != LSX_OK ||
+      check_prompt_sizes(*q, *k_pages, batch) != LSX_OK ||
+      check_table_size(max_pages, k_pages->N) != LSX_OK)
+    return 0;  // the call itself is refused, and says why
   return paged_fwd_workspace(*q, *k_pages, batch, max_pages, sm_count_or(kSmFallback));
 }
 
@@ -177,8 +218,7 @@ int attn_paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_ten
                    size_t workspace_bytes, lsx_stream_t stream) {
   LSX_TRY(check_pages(k_pages, v_pages));
   LSX_TRY(check_queries(q, k_pages, o, lse));
-  if (q->B != 1 || batch <= 0) return LSX_ERR_SHAPE;
-  if (batch > kMaxMapBatch || q->H / k_pages->H > 128) return LSX_ERR_UNSUPPORTED;
+  LSX_TRY(check_prompt_sizes(*q, *k_pages, batch));
   LSX_TRY(check_table(block_table, table_stride, max_pages, k_pages->N));
   LSX_TRY(check_ints(kv_lens));
   LSX_TRY(check_ints(cu_q));
