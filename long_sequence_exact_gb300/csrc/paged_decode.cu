@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const uint32_t smem0 = smem_addr(smem);
 
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column
-  float o[D / 8][4], m[2], l[2];
+  // (a CTA of a cluster that has no step leaves these as its part: no keys)
+  float o[D / 8][4] = {}, m[2] = {kNegInf, kNegInf}, l[2] = {};
   if (warp == kWarps) {
     // ---- loader: the page numbers of a step's 16-key groups, one per lane, are
     // fetched a step ahead; then one box per page, 64-column half and tensor
