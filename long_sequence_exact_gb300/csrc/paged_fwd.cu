@@ -658,6 +658,8 @@ __global__ void __launch_bounds__(384, 1)
           // m to the size of what the row has, or gets: alpha is at most 1 / l
           float m_new = fmaxf(l > 0.f ? m + lg2(l) : kNegInf, mx * sl2);
           if (!(m_new > kNegInf)) m_new = m;
+          // the weights stored first have landed before others follow them
+          tmem_st_wait();
           if (!first) {
             // O_t must hold the finished P_t V of the previous key tile
             if (!wait(&sm.o_full[t], s_phase)) { ok = false; break; }

@@ -1,4 +1,5 @@
-"""Paged attention where its state begins and ends: short units over a cluster."""
+"""Paged attention where its state begins and ends: short units over a cluster,
+a prompt's first key tile."""
 
 import pytest
 import torch
@@ -7,7 +8,7 @@ import long_sequence_exact_gb300 as lsx
 import paged_ref as P
 from helpers import check_close, check_lse, f64
 from long_sequence_exact_gb300.inputs import random_tensor
-from test_gpu_paged import DEV, P_SPLIT, decode_case, done, ints, poison
+from test_gpu_paged import DEV, P_BF16, P_SPLIT, decode_case, done, ints, poison, prompt_case
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,27 @@ def test_clusters_with_fewer_steps_than_blocks(d, hq, nq, level):
         assert done() == 0
         check_lse(f64(lse), l_ref, tol_lse)
         check_close(f64(o), o_ref, tol)
+
+
+@pytest.mark.parametrize("level", [60, -60])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_the_first_tile_formed_twice(d, level):
+    """Rows that end in their first tile, and first tiles whose scores lie far from
+    0, form their weights a second time in the same place: a weight left from the
+    first time would be 2^86 or 2^-86 times too large.  Thirty times the same bits."""
+    seqs = [(0, 100), (0, 1), (20, 60), (0, 0), (0, 700), (130, 40)]
+    q, kp, vp, table, lens, cu = prompt_case(4, 2, d, 16, seqs, seed=41)
+    level_scores(q, kp, level, d ** -0.5)
+    tol, tol_lse = P.tolerances(q, kp, vp, P_BF16, torch.float32)
+    tol_lse += 3 * P.U32 * abs(level) * 1.4427
+    o_ref, l_ref = P.fwd(q, kp, vp, table, lens, cu)
+    poison(kp, vp, table, lens, 16)
+    args = (q, kp, vp, table, ints(lens), ints(cu))
+    o, lse = lsx.paged_fwd(*args, out_dtype=torch.float32)
+    assert done() == 0
+    check_lse(f64(lse), l_ref, tol_lse)
+    check_close(f64(o), o_ref, tol)
+    for _ in range(30):
+        o2, lse2 = lsx.paged_fwd(*args, out_dtype=torch.float32)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert done() == 0
