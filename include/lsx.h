@@ -358,8 +358,9 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  * negative length as 0; each but the last records LSX_ERR_PAGE in the status
  * word.  Rows of a page past a sequence's length are never used, whatever
  * they hold.  The values before it have to be finite: an infinity or NaN there
- * can reach queries that do not see it (a weight of 0 times it).  A score that
- * is NaN or +infinity makes its query's O and LSE NaN.  All calls are
+ * can reach queries that do not see it (a weight of 0 times it); and 2^8 times
+ * the sum of |v| over a query's keys has to fit fp32 (weights of up to 2^8 are
+ * summed with V before the sum is divided by theirs).  A score that is NaN or +infinity makes its query's O and LSE NaN.  All calls are
  * inference-only (no gradients).
  *
  * attn_page_map -- one step's bookkeeping from the request lengths alone.

@@ -41,11 +41,15 @@
 //   descriptors move by their low words (919 -> 833 us).
 // - The softmax takes no maximum of a tile as a rule (833 -> 789 us, heads of 64
 //   5.0 -> 4.3 ms at 32768 tokens): the weights exp2(s - m) of any m give the same
-//   quotient as long as they neither overflow nor vanish.  m starts at 0; where a
-//   row's sum leaves [2^-32, 2^32] the tile's maximum is formed, m moved to the size
-//   of the sum, O rescaled and the tile's weights formed again.  Rows that end in
-//   their first tile take its maximum all the same: their largest weight is then
-//   exactly 1, and a row with one key is that key's value.
+//   quotient as long as neither they nor their products with V overflow or vanish.
+//   m starts at 0; where a tile's sum reaches 2^15 (128 weights of 2^8, which is how
+//   far the dense forward lets them go) or a row's is not above 1/2, the tile's
+//   maximum is formed, m moved to the size of the sum, O rescaled and the tile's
+//   weights formed again.  So |O| stays below 2^8 times the sum of |v|, and a small
+//   V keeps all but a bit of the range that weights under a maximum leave it (a
+//   window up to 2^8 instead: prompts 2.6% slower).  Rows that end in their first
+//   tile take its maximum all the same: their largest weight is then exactly 1, and
+//   a row with one key is that key's value.
 // - Query tile 1's first scores wait for tile 0's first softmax: the two stay out
 //   of step, each softmax under the other's products (789 -> 776 us).
 // Measured and not kept: P published in halves (a wait more: +7%, and nothing
@@ -77,8 +81,8 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMostSum = 4294967296.f;     // 2^32 (see the softmax)
-constexpr float kLeastSum = 2.3283064e-10f;  // 2^-32
+constexpr float kMostSum = 32768.f;  // 2^15 (see the softmax)
+constexpr float kLeastSum = 0.5f;
 constexpr int kOkRing = 8;       // >= stages + 2 (see the loader)
 constexpr int kItems = 4;        // items handed to the other roles ahead
 constexpr int kMinPiece = 4;     // key tiles

@@ -1,0 +1,112 @@
+"""Paged attention over the values that its documentation allows: scores whose
+level moves along the keys, large and small V."""
+
+import numpy as np
+import pytest
+import torch
+
+import long_sequence_exact_gb300 as lsx
+import paged_ref as P
+from helpers import check_close, check_lse, f64
+from test_gpu_paged import P_BF16, P_SPLIT, decode_case, done, ints, poison, prompt_case
+
+pytestmark = pytest.mark.gpu
+
+# every way through the two entry points: a call, its queries' weights' rounding
+PATHS = ["prompt", "chunk", "prefix_many", "prefix_few", "runs", "clusters"]
+
+
+class Path:
+    """A problem whose keys follow one another in `order`: (pages, page, row) of
+    the longest sequence's keys 0, 1, .. (behind the shared prefix, where there is one)."""
+
+    def __init__(self, name, d, keys, seed):
+        page, self.name = 16, name
+        if name in ("prompt", "chunk"):
+            new = keys if name == "prompt" else 5
+            c = prompt_case(4, 2, d, page, [(keys - new, new), (0, 30)], seed=seed)
+            self.q, self.kp, self.vp, self.table, self.lens, self.cu = c
+            self.prefix, self.prefix_len, self.p = [], 0, P_BF16
+            row, n = self.table[0].tolist(), keys
+        else:
+            b = {"prefix_many": 20, "prefix_few": 3}.get(name, 2)
+            self.prefix_len = keys if name.startswith("prefix") else 0
+            self.lens = [7, 0, 40] * 7 if self.prefix_len else [keys, 9]
+            self.lens = self.lens[:b]
+            c = decode_case(4, 2, 2, d, page, self.lens, self.prefix_len, seed, width=2600 if name == "runs" else None)
+            self.q, self.kp, self.vp, self.table, self.prefix = c
+            self.p = P_BF16 if name == "prefix_many" else P_SPLIT
+            row, n = (self.prefix, keys) if self.prefix_len else (self.table[0].tolist(), keys)
+        self.keys = [(row[i // page], i % page) for i in range(n)]
+
+    def levels(self, levels):
+        """Scores near levels[i] for key i of self.keys, near 0 for other keys
+        (natural logarithm; noise of about 1 stays)."""
+        d, big = self.q.shape[-1], max(1.0, max(abs(x) for x in levels))
+        a = (big / d ** 0.5) ** 0.5
+        self.q.copy_(self.q.float() * 0.05 + a)
+        k = self.kp.float() * 0.05
+        pages, rows = (torch.tensor(x, device=k.device) for x in zip(*self.keys))
+        k[pages, :, rows] += (torch.tensor(levels, device=k.device) / big * a)[:, None, None]
+        self.kp.copy_(k)
+        return big
+
+    def reference(self):
+        if self.name in ("prompt", "chunk"):
+            return P.fwd(self.q, self.kp, self.vp, self.table, self.lens, self.cu)
+        return P.decode(self.q, self.kp, self.vp, self.table, self.lens, self.prefix, self.prefix_len)
+
+    def run(self, dtype=torch.float32):
+        if self.name in ("prompt", "chunk"):
+            return lsx.paged_fwd(self.q, self.kp, self.vp, self.table, ints(self.lens), ints(self.cu), out_dtype=dtype)
+        return lsx.paged_decode(self.q, self.kp, self.vp, self.table, ints(self.lens),
+                                prefix_table=ints(self.prefix) if self.prefix_len else None,
+                                prefix_len=self.prefix_len, out_dtype=dtype)
+
+    def check(self, level=0.0, dtype=torch.float32, lost=0.0):
+        tol, tol_lse = P.tolerances(self.q, self.kp, self.vp, self.p, dtype)
+        tol += lost
+        # the maximum, its sum with the logarithm and the change of base: half a step of the level each
+        tol_lse += 3 * P.U32 * level * 1.4427
+        o_ref, l_ref = self.reference()
+        poison(self.kp, self.vp, self.table, self.lens, 16, self.prefix, self.prefix_len)
+        o, lse = self.run(dtype)
+        assert done() == 0
+        check_lse(f64(lse), l_ref, tol_lse)
+        check_close(f64(o), o_ref, tol)
+
+
+def profile(name, n):
+    x = np.linspace(0.0, 1.0, n)
+    tile = np.arange(n) // 128
+    return {"rise": 80 * x - 40, "fall": 40 - 80 * x, "steps": np.where(tile % 2 == 0, -30.0, 30.0),
+            "spike": np.where(tile == 2, 90.0, 0.0), "hole": np.where(tile == 1, -90.0, 0.0),
+            "overflow": np.where(tile >= 3, 200.0, -60.0), "climb": 9.0 * tile}[name].tolist()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("levels", ["rise", "fall", "steps", "spike", "hole", "overflow", "climb"])
+def test_levels_that_move_along_the_keys(path, d, levels):
+    """The reference that weights are formed against has to follow the scores, up
+    and down, tile by tile, with what was summed before it."""
+    n = 700
+    x = Path(path, d, n, 21)
+    x.check(x.levels(profile(levels, n)))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("level2", [24, 21, 9, 7, 0, -7, -9, -20, -36])  # base 2
+@pytest.mark.parametrize("exponent", [105, -114])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_and_small_values(path, d, level2, exponent, dtype):
+    """V of about 2^105, and of about 2^-114 and one sign, over 700 keys, whatever the
+    scores' level.  2^8 times the sum of |v| fits fp32.  A product below 2^-126 may
+    be lost: 700 of them, over weights whose sum is at least 1/2 a tile."""
+    x = Path(path, d, 700, 22)
+    if level2:
+        x.levels([level2 / 1.4427] * 700)
+    x.vp.copy_((x.vp.float() if exponent > 0 else x.vp.float().abs()) * 2.0 ** exponent)
+    assert 2.0 ** 8 * 700 * float(x.vp.float().abs().max()) < 2.0 ** 127
+    x.check(abs(level2) / 1.4427, dtype, lost=700 * 2.0 ** -126 / (0.5 * 700 / 128))
