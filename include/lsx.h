@@ -360,8 +360,9 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  * they hold.  The values before it have to be finite: an infinity or NaN there
  * can reach queries that do not see it (a weight of 0 times it); and 2^8 times
  * the sum of |v| over a query's keys has to fit fp32 (weights of up to 2^8 are
- * summed with V before the sum is divided by theirs).  A score that is NaN or +infinity makes its query's O and LSE NaN.  All calls are
- * inference-only (no gradients).
+ * summed with V before the sum is divided by theirs).  A score that is NaN or
+ * +infinity makes its query's O and LSE NaN.  All calls are inference-only (no
+ * gradients).
  *
  * attn_page_map -- one step's bookkeeping from the request lengths alone.
  *   ctx_lens, new_lens: int32 [batch] (1 <= batch <= 4096), the keys a
@@ -392,9 +393,9 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *   before its own (NULL when prefix_len is 0): a prefix shared by the batch,
  *   read once for up to 256 query rows together, not once per sequence.
  *   o [B, Hq, Nq, D] bf16 or f32, lse [B, Hq, Nq, 1] f32; a query without
- *   keys gets O = 0, LSE = -inf.  P is kept to 16 bits in the P V product; that
- *   of a prefix which more than 32 query rows of a kv head share, B * (Hq / Hkv)
- *   * Nq, is rounded to bf16.
+ *   keys gets O = 0, LSE = -inf.  P is kept to 16 bits in the P V product, but with
+ *   a bf16 o that of a prefix which more than 32 query rows of a kv head share,
+ *   B * (Hq / Hkv) * Nq, is rounded to bf16 (less of an error than o's own rounding).
  *
  * attn_paged_fwd -- prompts: ragged query tokens, causal, over the cache.
  *   q [1, Hq, T, D] bf16, the tokens of sequence b at [cu_q[b], cu_q[b + 1])

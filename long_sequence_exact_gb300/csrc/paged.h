@@ -82,7 +82,8 @@ int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const ls
 // Partials of every decode query against a prefix that all of them see, on
 // the prompt kernel: piece i of the row that is token (b, n) of head g of kv head
 // hk is row ((b / (2 tpt) * pieces + i) * Hkv + hk) * 256 + (b / tpt % 2) * 128 +
-// ((b % tpt) * Nq + n) * G + g of o [rows][D] and l [rows].
+// ((b % tpt) * Nq + n) * G + g of o [rows][D] and l [rows].  split_p: P to 16 bits
+// (else bf16).
 struct PrefixPlan {
   int tpt, pieces, size;  // sequences of a row tile; pieces of the prefix, key tiles each
   int64_t rows;           // of all pieces
@@ -90,8 +91,8 @@ struct PrefixPlan {
 PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, int sm_count);
 int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                   const PagedCache& prefix, int64_t prefix_len, const PrefixPlan& plan,
-                  float scale, float* part_o, float* part_l, const DeviceCtx& ctx,
-                  cudaStream_t s);
+                  float scale, bool split_p, float* part_o, float* part_l,
+                  const DeviceCtx& ctx, cudaStream_t s);
 // Ragged prompt tokens, causal, over the pages.
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
                            int64_t max_pages, int sm_count);

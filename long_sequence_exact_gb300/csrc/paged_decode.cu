@@ -22,7 +22,8 @@
 // by warp-level bf16 MMAs, 16 query rows (padded) x 16 keys a time; the four
 // compute warps share the step's keys (and, from 17 rows on, the row tiles).  P
 // enters the P V product as the sum of two bf16, so that the result keeps 16
-// bits of it: the tensor pipe is a quarter busy with it.
+// bits of it (up to 16 rows the tensor pipe is a quarter busy with it; each doubling
+// of the rows doubles that).
 //
 // Measured (8 kv heads of 128 under 32 query heads, ragged): 64 sequences of up
 // to 8192 keys 183 us, 6.5 TB/s, of up to 2048 keys 56 us; eight of 131072 keys,
@@ -772,7 +773,10 @@ RunLayout run_layout(int64_t slots, int64_t R, int64_t D, int64_t units, int64_t
   return x;
 }
 
-// More query rows than a warp kernel's CTA holds go to the prompt kernel.
+// A prefix under more query rows of a key head than these goes to the prompt kernel.
+// 131072 keys under 32, 36 and 64 rows, heads of 128: 105, 175 and 179 us here, 124
+// there (36 and 64), 162 with P to 16 bits; of 64: 64, 119 and 122 us here, 97 and
+// 140 there.  4096 keys differ by 2 us at most.
 constexpr int64_t kMaxWarpRows = 32;
 
 struct PageMaps {
@@ -947,7 +951,8 @@ int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const ls
       float* part_o = reinterpret_cast<float*>(ws);
       ws += align256(static_cast<size_t>(plan.rows * q.D) * 4);
       mp.tiles = TileView{plan.tpt, plan.pieces, part_o, part_l};
-      rc = launch_prefix(q, k_pages, v_pages, p.c, prefix_len, plan, scale, part_o, part_l, ctx, s);
+      rc = launch_prefix(q, k_pages, v_pages, p.c, prefix_len, plan, scale, o.dtype == LSX_F32,
+                         part_o, part_l, ctx, s);
     }
     if (rc != LSX_OK) return rc;
     p.c = c;

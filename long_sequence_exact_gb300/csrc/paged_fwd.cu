@@ -28,8 +28,16 @@
 // sequence's last key, warps 4..7 and 8..11 do the softmax of query tile 0 and 1
 // (thread = row = TMEM lane).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D); P_t (bf16)
-// replaces S_t.  The MMA order per key tile j is P_0 V_j, S_0(j+1), P_1 V_j,
+// replaces S_t's first half.  The MMA order per key tile j is P_0 V_j, S_0(j+1), P_1 V_j,
 // S_1(j+1): each tile's softmax runs under two products of the other.
+//
+// Bits of P.  It is rounded to bf16 once, as in the dense forward (the row sums
+// are of the weights before that): the error this leaves in O is below that of a
+// bf16 O itself.  A shared prefix whose results are f32 keeps 16 bits, as decode does
+// everywhere else, so that their accuracy does not depend on how many others are
+// in the batch: P = bf16(P) + bf16(P - bf16(P)), the second half behind the first
+// in S_t's columns and multiplied with V as well.  131072 keys under 128 rows, a
+// call: heads of 128 124 us with one product, 161 with both, of 64 98 and 141.
 //
 // The issuing thread and the softmax take turns in setting the pace, so both are
 // kept short (times of the 12345 tokens above, one after the other):
@@ -253,7 +261,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
-template <int D>
+template <int D, bool kSplitP>
 __global__ void __launch_bounds__(384, 1)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
@@ -455,6 +463,12 @@ __global__ void __launch_bounds__(384, 1)
         for (int kk = 0; kk < 8; ++kk)
           mma_ts_lo(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
                     v0 + static_cast<uint32_t>(mnmajor_step(kk)), v_hi, kIdO, kk > 0 ? 1u : acc0);
+        if constexpr (kSplitP) {  // what P's rounding left out, from the columns behind
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_lo(tmem + 256 + t * 128, tmem + t * 128 + 64 + kk * 8,
+                      v0 + static_cast<uint32_t>(mnmajor_step(kk)), v_hi, kIdO, 1u);
+        }
         mma_commit(&sm.o_full[t]);
       };
       for (uint32_t r = 0;; ++r) {
@@ -630,6 +644,24 @@ __global__ void __launch_bounds__(384, 1)
           const float2 sc2 = make_float2(sl2, sl2);
           const float2 nm2 = make_float2(-m, -m);
           float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+          if constexpr (kSplitP) {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 arg =
+                    __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
+                const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
+                if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
+                hi[i] = pack_bf16(e.x, e.y);
+                lo[i] = pack_bf16(e.x - __uint_as_float(hi[i] << 16),
+                                  e.y - __uint_as_float(hi[i] & 0xffff0000u));
+              }
+              tmem_st16(tS + cc * 16, hi);
+              tmem_st16(tS + 64 + cc * 16, lo);
+            }
+          } else {
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             uint32_t pk[32];
@@ -642,6 +674,7 @@ __global__ void __launch_bounds__(384, 1)
               pk[i] = pack_bf16(e.x, e.y);
             }
             tmem_st32(tS + cc * 32, pk);
+          }
           }
           return (la.x + la.y) + (lb.x + lb.y);
         };
@@ -1083,12 +1116,12 @@ bool encode_pages(CUtensorMap* map, const lsx_tensor& t) {
                  static_cast<uint32_t>(t.N < 128 ? t.N : 128), 1, 1);
 }
 
-template <int D>
+template <int D, bool kSplitP>
 int launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                  const FwdParams& p, int64_t grid, bool early, int device, cudaStream_t s) {
   const size_t smem = sizeof(Smem<D>) + 1024;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(paged_fwd_kernel<D>, static_cast<int>(smem), device, done)) return LSX_ERR_LAUNCH;
+  if (!allow_smem(paged_fwd_kernel<D, kSplitP>, static_cast<int>(smem), device, done)) return LSX_ERR_LAUNCH;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(384);
@@ -1100,7 +1133,7 @@ int launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
   cfg.attrs = &attr;
   cfg.numAttrs = early ? 1 : 0;
   timing_begin(kKidPagedFwd, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D>, tq, tk, tv, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_fwd_kernel<D, kSplitP>, tq, tk, tv, p);
   timing_end(kKidPagedFwd, s);
   return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
 }
@@ -1155,8 +1188,8 @@ PrefixPlan prefix_plan(int64_t B, int64_t per, int64_t hkv, int64_t prefix_len, 
 
 int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                   const PagedCache& prefix, int64_t prefix_len, const PrefixPlan& plan,
-                  float scale, float* part_o, float* part_l, const DeviceCtx& ctx,
-                  cudaStream_t s) {
+                  float scale, bool split_p, float* part_o, float* part_l,
+                  const DeviceCtx& ctx, cudaStream_t s) {
   FwdParams p;
   p.c = prefix;
   p.Hkv = k_pages.H;
@@ -1185,8 +1218,9 @@ int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tens
     return LSX_ERR_LAUNCH;
   const int64_t items = plan.rows / 256;
   const int64_t grid = items < ctx.sm_count ? items : ctx.sm_count;
-  return q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, false, ctx.device, s)
-                    : launch_tiles<64>(tq, tk, tv, p, grid, false, ctx.device, s);
+  auto launch = q.D == 128 ? (split_p ? launch_tiles<128, true> : launch_tiles<128, false>)
+                           : (split_p ? launch_tiles<64, true> : launch_tiles<64, false>);
+  return launch(tq, tk, tv, p, grid, false, ctx.device, s);
 }
 
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
@@ -1249,8 +1283,8 @@ int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_t
   if (cudaGetLastError() != cudaSuccess) return LSX_ERR_LAUNCH;
   const int64_t most = x.max_entries * p.Hkv;
   const int64_t grid = most < ctx.sm_count ? most : ctx.sm_count;
-  const int rc = q.D == 128 ? launch_tiles<128>(tq, tk, tv, p, grid, true, ctx.device, s)
-                            : launch_tiles<64>(tq, tk, tv, p, grid, true, ctx.device, s);
+  const int rc = q.D == 128 ? launch_tiles<128, false>(tq, tk, tv, p, grid, true, ctx.device, s)
+                            : launch_tiles<64, false>(tq, tk, tv, p, grid, true, ctx.device, s);
   if (rc != LSX_OK || x.max_slots == 0) return rc;
   const FwdMergeParams mp{pp.header, pp.cut, p.Hkv, p.G, p.tpt, p.part_o, p.part_l, o, lse};
   cudaLaunchConfig_t cfg{};

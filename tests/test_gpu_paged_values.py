@@ -35,7 +35,7 @@ class Path:
             self.lens = self.lens[:b]
             c = decode_case(4, 2, 2, d, page, self.lens, self.prefix_len, seed, width=2600 if name == "runs" else None)
             self.q, self.kp, self.vp, self.table, self.prefix = c
-            self.p = P_BF16 if name == "prefix_many" else P_SPLIT
+            self.p = P_SPLIT
             row, n = (self.prefix, keys) if self.prefix_len else (self.table[0].tolist(), keys)
         self.keys = [(row[i // page], i % page) for i in range(n)]
 
@@ -64,7 +64,8 @@ class Path:
                                 prefix_len=self.prefix_len, out_dtype=dtype)
 
     def check(self, level=0.0, dtype=torch.float32, lost=0.0):
-        tol, tol_lse = P.tolerances(self.q, self.kp, self.vp, self.p, dtype)
+        p = P_BF16 if self.name == "prefix_many" and dtype is torch.bfloat16 else self.p
+        tol, tol_lse = P.tolerances(self.q, self.kp, self.vp, p, dtype)
         tol += lost
         # the maximum, its sum with the logarithm and the change of base: half a step of the level each
         tol_lse += 3 * P.U32 * level * 1.4427
@@ -110,3 +111,23 @@ def test_large_and_small_values(path, d, level2, exponent, dtype):
     x.vp.copy_((x.vp.float() if exponent > 0 else x.vp.float().abs()) * 2.0 ** exponent)
     assert 2.0 ** 8 * 700 * float(x.vp.float().abs().max()) < 2.0 ** 127
     x.check(abs(level2) / 1.4427, dtype, lost=700 * 2.0 ** -126 / (0.5 * 700 / 128))
+
+
+@pytest.mark.parametrize("batch,hq,hkv,nq", [(2, 8, 2, 1), (8, 4, 1, 1), (9, 8, 2, 1), (40, 2, 2, 1), (3, 8, 2, 5),
+                                             (16, 4, 1, 4), (5, 16, 2, 8), (130, 6, 2, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("prefix_len", [16, 100, 1000])
+def test_f32_results_behind_a_prefix_keep_16_bits_of_the_weights(batch, hq, hkv, nq, d, prefix_len):
+    """8 to 390 query rows a key head.  A small scale keeps the scores' own error
+    far below a bf16 rounding of P, so that the bound sees one."""
+    lens = [0, 3, 20][:batch] + [0] * (batch - 3)
+    q, kp, vp, table, prefix = decode_case(hq, hkv, nq, d, 16, lens, prefix_len, seed=23)
+    scale = 0.002
+    tol, tol_lse = P.tolerances(q, kp, vp, P_SPLIT, torch.float32, scale)
+    assert tol < 2 * 2.0 ** -14 * float(vp.float().abs().max())
+    o_ref, l_ref = P.decode(q, kp, vp, table, lens, prefix, prefix_len, scale)
+    poison(kp, vp, table, lens, 16, prefix, prefix_len)
+    o, lse = lsx.paged_decode(q, kp, vp, table, ints(lens), scale, ints(prefix), prefix_len, out_dtype=torch.float32)
+    assert done() == 0
+    check_lse(f64(lse), l_ref, tol_lse)
+    check_close(f64(o), o_ref, tol)
