@@ -20,10 +20,10 @@ class Path:
     """A problem whose keys follow one another in `order`: (pages, page, row) of
     the longest sequence's keys 0, 1, .. (behind the shared prefix, where there is one)."""
 
-    def __init__(self, name, d, keys, seed):
+    def __init__(self, name, d, keys, seed, new=None):
         page, self.name = 16, name
         if name in ("prompt", "chunk"):
-            new = keys if name == "prompt" else 5
+            new = (new or keys) if name == "prompt" else 5
             c = prompt_case(4, 2, d, page, [(keys - new, new), (0, 30)], seed=seed)
             self.q, self.kp, self.vp, self.table, self.lens, self.cu = c
             self.prefix, self.prefix_len, self.p = [], 0, P_BF16
@@ -51,15 +51,16 @@ class Path:
         self.kp.copy_(k)
         return big
 
-    def reference(self):
+    def reference(self, scale=None):
         if self.name in ("prompt", "chunk"):
-            return P.fwd(self.q, self.kp, self.vp, self.table, self.lens, self.cu)
-        return P.decode(self.q, self.kp, self.vp, self.table, self.lens, self.prefix, self.prefix_len)
+            return P.fwd(self.q, self.kp, self.vp, self.table, self.lens, self.cu, scale)
+        return P.decode(self.q, self.kp, self.vp, self.table, self.lens, self.prefix, self.prefix_len, scale)
 
-    def run(self, dtype=torch.float32):
+    def run(self, dtype=torch.float32, scale=None):
         if self.name in ("prompt", "chunk"):
-            return lsx.paged_fwd(self.q, self.kp, self.vp, self.table, ints(self.lens), ints(self.cu), out_dtype=dtype)
-        return lsx.paged_decode(self.q, self.kp, self.vp, self.table, ints(self.lens),
+            return lsx.paged_fwd(self.q, self.kp, self.vp, self.table, ints(self.lens), ints(self.cu), scale,
+                                 out_dtype=dtype)
+        return lsx.paged_decode(self.q, self.kp, self.vp, self.table, ints(self.lens), scale,
                                 prefix_table=ints(self.prefix) if self.prefix_len else None,
                                 prefix_len=self.prefix_len, out_dtype=dtype)
 
@@ -131,3 +132,37 @@ def test_f32_results_behind_a_prefix_keep_16_bits_of_the_weights(batch, hq, hkv,
     assert done() == 0
     check_lse(f64(lse), l_ref, tol_lse)
     check_close(f64(o), o_ref, tol)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_page_of_values_counts_in_a_long_row(path, d):
+    """Rows over 6000 keys, each held to a bound of its own size.  With weights
+    rounded by u independently, the error of a row of O has a root mean square of at
+    most u sqrt(sum_j p_j^2 |v_j|^2) <= u max|v| sqrt(sum_j p_j^2); four times that is
+    allowed, and what an error of the scores themselves can do.  At this scale the
+    weights are nearly equal, and 16 keys' values in the place of others change a row by
+    more than twice its bound (shown on the reference, with a page of V swapped): less
+    the error that a right result may have, still more than the bound."""
+    scale, n = 0.002, 6000
+    x = Path(path, d, n, 24, new=150)
+    o_ref, l_ref = x.reference(scale)
+    squares = np.exp(x.reference(2 * scale)[1] - 2 * l_ref)   # sum_j p_j^2 of each row
+    vmax = float(x.vp.float().norm(dim=-1).max())
+    rel = P.score_error(x.q, x.kp, scale) + 2.0 ** -19 + 2.0 ** -21 + 2.0 ** -19
+    bound = 4 * x.p * vmax * np.sqrt(squares) + 2 * rel * vmax
+    long = squares < 1.5 / n                                   # rows that see all of the longest sequence
+    assert long.sum() >= 8
+    kept = x.vp.clone()
+    a, b = x.keys[3008][0], x.keys[16][0]
+    x.vp[a] = kept[b]
+    planted = np.linalg.norm(x.reference(scale)[0] - o_ref, axis=-1)
+    assert (planted[long] > 2 * bound[long]).all()
+    x.vp.copy_(kept)
+    poison(x.kp, x.vp, x.table, x.lens, 16, x.prefix, x.prefix_len)
+    o, lse = x.run(scale=scale)
+    assert done() == 0
+    fin = np.isfinite(l_ref)
+    error = np.linalg.norm(f64(o) - o_ref, axis=-1)
+    assert (error[fin] <= bound[fin]).all(), float((error[fin] / bound[fin]).max())
+    check_lse(f64(lse), l_ref, rel + 2.0 ** -19)
