@@ -1,5 +1,5 @@
 """Paged attention where its state begins and ends: short units over a cluster,
-a prompt's first key tile."""
+a prompt's first key tile, the streams that calls run on, and refusals."""
 
 import pytest
 import torch
@@ -70,3 +70,99 @@ def test_weights_of_the_first_tile_formed_twice(d, level):
         o2, lse2 = lsx.paged_fwd(*args, out_dtype=torch.float32)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert done() == 0
+
+
+def steps(q, kp, vp, table, lens, prefix, packed, cu, rows, slots, free):
+    """One call of every paged entry point, each form of decode among them; no copy
+    from the host, which would wait for the stream."""
+    got = list(lsx.page_map(table.clone(), lens, torch.ones_like(lens), free, 16, 5))
+    lsx.page_append(rows, rows, kp, vp, slots)
+    for width in (table, torch.nn.functional.pad(table, (0, 2500), value=-1)):
+        got += lsx.paged_decode(q, kp, vp, width, lens)
+    for n in (1, 40):                                  # few query rows behind a prefix, and many
+        qq, tt, ll = q.repeat(n, 1, 1, 1), table.repeat(n, 1), lens.repeat(n)
+        got += lsx.paged_decode(qq, kp, vp, tt, ll, prefix_table=prefix, prefix_len=100)
+    return got + list(lsx.paged_fwd(packed, kp, vp, table, lens, cu))
+
+
+def test_calls_run_on_the_current_stream_alone():
+    """While the default stream is held by a delay (a second or so), calls on another
+    stream finish; they would not if any of their launches went to the default
+    stream or waited for it.  And calls on the held stream wait behind the delay."""
+    q, kp, vp, table, prefix = decode_case(4, 2, 1, 128, 16, [500, 3], 100)
+    lens, prefix, cu = ints([500, 3]), ints(prefix), ints([0, 60, 63])
+    packed = random_tensor((63, 4, 128), 7, device=DEV).transpose(0, 1)[None]
+    rows, slots = random_tensor((1, 2, 3, 128), 8, device=DEV), ints([3, -1, 17], torch.int64)
+    args = (q, kp, vp, table, lens, prefix, packed, cu, rows, slots, ints(list(range(9))))
+    want = steps(*args)                                # (and everything loaded and allocated once)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        steps(*args)
+    assert done() == 0
+    delay = 2_000_000_000                              # clock cycles
+    other = torch.zeros(8, device=DEV)
+    torch.cuda.synchronize()
+    held = torch.cuda.Event()
+    torch.cuda._sleep(delay)
+    other.fill_(1.0)
+    held.record()
+    with torch.cuda.stream(side):
+        got = steps(*args)
+    side.synchronize()
+    assert not held.query(), "the calls did not run beside the held stream"
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    ready = torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(delay)
+        steps(*args)
+        ready.record()
+    torch.cuda.default_stream().synchronize()
+    assert not ready.query(), "a call on the held stream did not wait"
+    assert done() == 0
+
+
+SHAPE, WORKSPACE, ALIGN, UNSUPPORTED = -2, -6, -4, -5
+
+
+@pytest.mark.parametrize("prefix_len", [0, 100])
+def test_refusals_of_outputs_and_workspaces(prefix_len):
+    """Each wrong thing by itself, by its code; the right call beside it runs."""
+    q, kp, vp, table, prefix = decode_case(4, 2, 1, 128, 16, [50, 3], prefix_len, width=2500)
+    pre = dict(prefix_table=ints(prefix), prefix_len=prefix_len) if prefix_len else {}
+    call = lambda **kw: lsx.paged_decode(q, kp, vp, table, ints([50, 3]), **pre, **kw)  # noqa: E731
+    need = lsx.paged_decode_workspace_size(q, kp, 2500, prefix_len)
+    assert need > 256
+    room = torch.empty(need + 512, dtype=torch.uint8, device=DEV)
+    room = room[(-room.data_ptr()) % 256:]
+    out = lambda d, t=torch.bfloat16: torch.empty((2, 4, 1, d), dtype=t, device=DEV)  # noqa: E731
+    for code, kw in ((SHAPE, dict(out=out(64))), (WORKSPACE, dict(workspace=room[:need - 1])),
+                     (WORKSPACE, dict(workspace=room[:1])), (ALIGN, dict(workspace=room[16:16 + need])),
+                     (SHAPE, dict(lse=torch.empty((2, 4, 2), device=DEV))),
+                     (ALIGN, dict(out=torch.empty(2 * 4 * 128 + 4, dtype=torch.bfloat16, device=DEV)[4:].view(2, 4, 1, 128)))):
+        with pytest.raises(lsx._lib.LsxError) as e:
+            call(**kw)
+        assert e.value.code == code, kw.keys()
+    want = call()
+    got = call(out=out(128), workspace=room[:need])
+    assert done() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_refusals_of_prompt_outputs_and_workspaces():
+    q, kp, vp, table, lens, cu = prompt_case(4, 2, 64, 16, [(600, 40), (0, 9)])
+    call = lambda **kw: lsx.paged_fwd(q, kp, vp, table, ints(lens), ints(cu), **kw)  # noqa: E731
+    need = lsx.paged_fwd_workspace_size(q, kp, 2, table.shape[1])
+    room = torch.empty(need + 512, dtype=torch.uint8, device=DEV)
+    room = room[(-room.data_ptr()) % 256:]
+    for code, kw in ((SHAPE, dict(out=torch.empty((1, 4, 49, 128), dtype=torch.bfloat16, device=DEV))),
+                     (WORKSPACE, dict(workspace=room[:need - 1])), (ALIGN, dict(workspace=room[16:16 + need])),
+                     (SHAPE, dict(lse=torch.empty((1, 4, 48), device=DEV)))):
+        with pytest.raises(lsx._lib.LsxError) as e:
+            call(**kw)
+        assert e.value.code == code, kw.keys()
+    want = call()
+    got = call(workspace=room[:need])
+    assert done() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
