@@ -354,15 +354,16 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  * Lengths, tables and slots are read on the device when the call runs, so a
  * captured graph follows their contents.  What the host cannot check is
  * checked there: a page number outside [0, P) leaves its keys out (as if
- * masked), a length beyond the table counts as max_pages * page keys, a
- * negative length as 0; each but the last records LSX_ERR_PAGE in the status
- * word.  Rows of a page past a sequence's length are never used, whatever
- * they hold.  The values before it have to be finite: an infinity or NaN there
- * can reach queries that do not see it (a weight of 0 times it); and 2^8 times
- * the sum of |v| over a query's keys has to fit fp32 (weights of up to 2^8 are
- * summed with V before the sum is divided by theirs).  A score that is NaN or
- * +infinity makes its query's O and LSE NaN.  All calls are inference-only (no
- * gradients).
+ * masked), a length beyond the table stands for the max_pages * page keys that
+ * there are (its queries keep their places behind them), a negative length for
+ * 0; each but the last records LSX_ERR_PAGE in the status word.  Rows of a page
+ * past a sequence's length are never used, whatever they hold.  The values
+ * before it have to be finite: an infinity or NaN there can reach queries that
+ * do not see it (a weight of 0 times it); and 2^8 times the sum of |v| over a
+ * query's keys has to fit fp32 (weights of up to 2^8 are summed with V before
+ * the sum is divided by theirs).  A score that is NaN or +infinity makes its
+ * query's O and LSE NaN.  What a call writes must not overlap what it reads (a
+ * page map's block table is both).  All calls are inference-only (no gradients).
  *
  * attn_page_map -- one step's bookkeeping from the request lengths alone.
  *   ctx_lens, new_lens: int32 [batch] (1 <= batch <= 4096), the keys a
@@ -387,7 +388,7 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *   tokens with one slot either may remain, in pieces.
  *
  * attn_paged_decode -- one or a few query tokens per sequence.
- *   q [B, Hq, Nq, D] bf16, (Hq / Hkv) * Nq <= 64; query n of sequence b sees
+ *   q [B, Hq, Nq, D] bf16, B < 65536, (Hq / Hkv) * Nq <= 64; query n of sequence b sees
  *   its keys j <= kv_len - Nq + n (the Nq tokens are its last ones).
  *   prefix_table: int32, the pages of prefix_len keys that every query sees
  *   before its own (NULL when prefix_len is 0): a prefix shared by the batch,
@@ -404,7 +405,8 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  *   that belong to no sequence are left as they were.  P is rounded to bf16.
  *
  * Both need the workspace their *_workspace_size names (256-byte aligned); 0 where
- * the sizes are refused, which the call then says.
+ * the sizes are refused, which the call then says.  A workspace belongs to one
+ * call, or one replay of a graph, at a time.
  * ---------------------------------------------------------------------- */
 int attn_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int64_t batch,
                   const int32_t* free_pages, int64_t n_free, int64_t page_size,

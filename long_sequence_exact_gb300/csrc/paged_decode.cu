@@ -27,7 +27,10 @@
 //
 // Measured (8 kv heads of 128 under 32 query heads, ragged): 64 sequences of up
 // to 8192 keys 183 us, 6.5 TB/s, of up to 2048 keys 56 us; eight of 131072 keys,
-// four drafts, 16 heads of 64, 330 us, 6.7 TB/s; one of 2049 keys 9.4 us.
+// four drafts, 16 heads of 64, 330 us, 6.7 TB/s; one of 2049 keys 9.6 us.  The 64
+// sequences of up to 8192 keys with 4, 32, 40 and 64 rows a key head: 185, 222, 384 and
+// 398 us.  From 33 rows on each warp multiplies every key of a step for its 16 rows,
+// and the warp MMAs (tensor pipe 51% busy, HBM 42%) set the time.
 #include <math.h>
 
 #include "paged.h"
@@ -789,7 +792,8 @@ constexpr int kSmem =
 static_assert(2 * (kSmem<128> + 1024) <= 228 * 1024, "shared memory of two CTAs");
 
 // Units a cluster each: all of them on the device at once, and short (the
-// table's width bounds the keys).  8 units of 128: 2048 keys 8.6 us, 13.6 us as
+// table's width bounds the keys; the lengths are not known here, so that a short
+// sequence behind a wide table takes runs: 2049 keys 13.8 us instead of 9.6).  8 units of 128: 2048 keys 8.6 us, 13.6 us as
 // runs; 8192 keys 20.0 and 17.1 us; of 64: 8192 keys 10.0 and 13.5 us, 16384 keys
 // 15.7 and 15.1 us.
 constexpr int kCluster = 8;

@@ -5,10 +5,14 @@
 // computation), with pages in the place of chunks.
 //
 // Bound: the tensor cores (4 D operations per visible (query, key) pair), for
-// few tokens the cache's bytes.  32 query and 8 kv heads of 128: 12345 tokens
-// 0.772 ms, 1.62 PFLOP/s; 32768 tokens 5.50 ms, 1.60 PFLOP/s; 512 tokens after 65536
-// keys 0.380 ms, of which the partials' merge 0.011; heads of 64, 32768 tokens
-// 4.36 ms, 1.01 PFLOP/s.
+// few tokens the cache's bytes.  32 query and 8 kv heads of 128, replayed from a
+// graph: 12345 tokens 0.778 ms, 1.60 PFLOP/s (0.82 after some seconds, when the power
+// cap lowers the clock); 32768 tokens 5.43 to 5.61 ms, 1.62 to 1.57 PFLOP/s; 512 tokens
+// after 65536 keys 0.364 to 0.383 ms, of which the partials' merge 0.011; heads of
+// 64, 32768 tokens 4.36 ms, 1.01 PFLOP/s.  With heads of 128 the tensor pipe is busy
+// 66% of the time; with heads of 64, half the products for the same weights, it and
+// the exponentials' pipe are at 39% and issue slots at 44%: the softmax's chain,
+// two warps a scheduler, sets the time.
 //
 // Rows.  The heads that share a key head are rows of one tile: row r of a
 // 128-row query tile is head r % G of token r / G, floor(128 / G) tokens a tile,

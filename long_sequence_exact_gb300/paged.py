@@ -17,7 +17,8 @@ One serving step:
     o, lse = paged_decode(q, k_pages, v_pages, block_table, kv_lens)
 
 Tensors live on the current CUDA device; calls are enqueued on the current
-stream.  Inference only: no gradients are recorded.  A page number, slot or
+stream.  A workspace, where one is given, belongs to one call (or one replay of a
+graph) at a time.  Inference only: no gradients are recorded.  A page number, slot or
 length outside the cache is skipped on the device and reported by
 ``sync_status`` (LSX_ERR_PAGE).
 """
