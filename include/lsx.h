@@ -359,10 +359,10 @@ int attn_decode_tree(const lsx_tensor* q, const lsx_tensor* pk, const lsx_tensor
  * 0; each but the last records LSX_ERR_PAGE in the status word.  Rows of a page
  * past a sequence's length are never used, whatever they hold.  The values
  * before it have to be finite: an infinity or NaN there can reach queries that
- * do not see it (a weight of 0 times it); and 2^8 times the sum of |v| over a
- * query's keys has to fit fp32 (weights of up to 2^8 are summed with V before
- * the sum is divided by theirs).  A score that is NaN or +infinity makes its
- * query's O and LSE NaN.  What a call writes must not overlap what it reads (a
+ * do not see it (a weight of 0 times it); and 2^8 n |v|, n the keys that a
+ * query sees, rounded up to 128, has to stay below 2^127 (weights whose sum is
+ * up to 2^15 a 128 keys are added up with V before the division by their sum).
+ * A score that is NaN or +infinity makes its query's O and LSE NaN.  What a call writes must not overlap what it reads (a
  * page map's block table is both).  All calls are inference-only (no gradients).
  *
  * attn_page_map -- one step's bookkeeping from the request lengths alone.

@@ -54,11 +54,11 @@
 // - The softmax takes no maximum of a tile as a rule (833 -> 789 us, heads of 64
 //   5.0 -> 4.3 ms at 32768 tokens): the weights exp2(s - m) of any m give the same
 //   quotient as long as neither they nor their products with V overflow or vanish.
-//   m starts at 0; where a tile's sum reaches 2^15 (128 weights of 2^8, which is how
-//   far the dense forward lets them go) or a row's is not above 1/2, the tile's
+//   m starts at 0; where a tile's sum reaches 2^15 (128 weights of 2^8: as far as
+//   the dense forward lets them go) or a row's is not above 1/2, the tile's
 //   maximum is formed, m moved to the size of the sum, O rescaled and the tile's
-//   weights formed again.  So |O| stays below 2^8 times the sum of |v|, and a small
-//   V keeps all but a bit of the range that weights under a maximum leave it (a
+//   weights formed again.  So |O| stays below 2^15 max |v| a tile, and a small V
+//   keeps all but a bit of the range that weights under a maximum leave it (a
 //   window up to 2^8 instead: prompts 2.6% slower).  Rows that end in their first
 //   tile take its maximum all the same: their largest weight is then exactly 1, and
 //   a row with one key is that key's value.

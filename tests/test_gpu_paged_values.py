@@ -104,14 +104,32 @@ def test_levels_that_move_along_the_keys(path, d, levels):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_large_and_small_values(path, d, level2, exponent, dtype):
     """V of about 2^105, and of about 2^-114 and one sign, over 700 keys, whatever the
-    scores' level.  2^8 times the sum of |v| fits fp32.  A product below 2^-126 may
+    scores' level.  2^8 n |v|, n = 768, is below 2^127.  A product below 2^-126 may
     be lost: 700 of them, over weights whose sum is at least 1/2 a tile."""
     x = Path(path, d, 700, 22)
     if level2:
         x.levels([level2 / 1.4427] * 700)
     x.vp.copy_((x.vp.float() if exponent > 0 else x.vp.float().abs()) * 2.0 ** exponent)
-    assert 2.0 ** 8 * 700 * float(x.vp.float().abs().max()) < 2.0 ** 127
+    assert 2.0 ** 8 * 768 * float(x.vp.float().abs().max()) < 2.0 ** 127
     x.check(abs(level2) / 1.4427, dtype, lost=700 * 2.0 ** -126 / (0.5 * 700 / 128))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("level2", [14, 16])  # base 2: below and above what moves the reference
+def test_one_heavy_key_of_every_tile_with_large_values(path, d, level2):
+    """All of a tile's weight on one key, whose values are the large ones."""
+    n = 700
+    x = Path(path, d, n, 25)
+    levels = [level2 / 1.4427 if i % 128 == 77 else 0.0 for i in range(n)]
+    big = x.levels(levels)
+    pages, rows = (torch.tensor(t, device=x.vp.device) for t in zip(*x.keys))
+    heavy = torch.tensor([105.0 if i % 128 == 77 else 0.0 for i in range(n)], device=x.vp.device)
+    v = x.vp.float()
+    v[pages, :, rows] *= (2.0 ** heavy)[:, None, None]
+    x.vp.copy_(v)
+    assert 2.0 ** 8 * 768 * float(x.vp.float().abs().max()) < 2.0 ** 127
+    x.check(big)
 
 
 @pytest.mark.parametrize("batch,hq,hkv,nq", [(2, 8, 2, 1), (8, 4, 1, 1), (9, 8, 2, 1), (40, 2, 2, 1), (3, 8, 2, 5),
