@@ -311,10 +311,11 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 // (105 before; bf16, twice the bytes: 76), tensor pipe 20%, issue 47%; 131072 keys under
 // 256 rows, 8 heads of 128: 129 us (147; bf16 108), tensor pipe 44%.
 // The rows' powers of two stay out of the softmax's loop:
-// - A tile's rows become value * 2^(e - E), E the largest exponent of the tile's rows
-//   (exact down to e = E - 15, and below that to 2^-33 of the largest that 2^E allows).
-//   For keys 2^E is a factor of all the tile's scores, for values an exponent of all its
-//   weights.
+// - A tile's rows become value * 2^(e - E + kRise), E the largest exponent of the tile's
+//   rows: at most 448 * 2^7, an f16 still, exact down to e = E - 22, and below that to
+//   half of f16's last step, 2^(E - 32) in all (a row's largest value is above 224 * 2^e).
+//   For keys 2^(E - kRise) is a factor of all the tile's scores, for values an exponent of
+//   all its weights.
 // - Q becomes f16 times a power of two that brings the largest element of an item's
 //   rows to [2^14, 2^15): 8 bits are kept exactly down to 2^-29 of it.
 // - P is kept as f16, 11 bits.  The weights that are stored are 2^kShift of what the row
@@ -323,13 +324,19 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 //   weight would be stored as more than 2^15.  f32 results: a weight's remainder is a
 //   second f16.
 constexpr int kShift = 8;
+constexpr int kRise = 7;
 
 // A tile [128][D] of e4m3 (rows of 128 bytes with the 128-byte swizzle, of 64 without)
-// to the f16 tile that the products read; thread t of 128.  Rows that are not in `live`
-// (one bit for the thread's four) become zeros.  A quarter of a warp's 16-byte accesses
-// have to fall on different banks, in the 8-bit tile (16 values of four columns' pieces
-// in a row) and in the f16 one (two pieces): its eight threads take half a row each of
-// two rows that differ in bits 0 and 2 (heads of 64: in bit 0).
+// to the f16 tile that the products read; thread t of 128.  `there`: a bit for each of the
+// thread's four rows; `clear`: those that are not become zeros.  A quarter of a warp's
+// 16-byte accesses have to fall on different banks, in the 8-bit tile (16 values of four
+// columns' pieces in a row) and in the f16 one (two pieces): its eight threads take half a
+// row each of two rows that differ in bits 0 and 2 (heads of 64: in bit 0).
+//
+// A row's power of two is an f16 factor.  f16 has those down to 2^-24 and the smallest
+// value is 2^-9, so that the first product stops at 2^-14, where it is exact; rows below
+// that (rare: 2^22 smaller than the tile's largest) are multiplied once more, where the one
+// rounding is.
 template <int D>
 __device__ __forceinline__ int widen_row(int t) {
   const int pair = (t >> 3) & 3, sel = (t >> 2) & 1;
@@ -337,20 +344,24 @@ __device__ __forceinline__ int widen_row(int t) {
 }
 template <int D>
 __device__ __forceinline__ void widen_tile(const uint8_t* src, const uint8_t* exps, int top,
-                                           uint32_t live, __nv_bfloat16* dst, int t) {
+                                           uint32_t there, bool clear, __nv_bfloat16* dst,
+                                           int t) {
   const int c = t & 3, r = widen_row<D>(t), sw = r & 7;
   const uint8_t* in = src + r * D;
   uint8_t* out = reinterpret_cast<uint8_t*>(dst) + r * 128;
   const int at0 = ((2 * c) ^ sw) << 4, at1 = ((2 * c + 1) ^ sw) << 4;
+  int least = 1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i, in += 8 * D, out += 8 * 128, live >>= 1) {
+  for (int i = 0; i < 4; ++i, in += 8 * D, out += 8 * 128, there >>= 1) {
     uint4 x[D / 64];
 #pragma unroll
     for (int half = 0; half < D / 64; ++half)
       x[half] = *reinterpret_cast<const uint4*>(in + ((D == 128 ? (half * 4 + c) ^ sw : c) << 4));
-    const float f1 = q8_power(max(static_cast<int>(exps[r + 8 * i]) - top, -126));
-    uint32_t f = pack_f16(f1, f1);
-    if ((live & 1u) == 0) {
+    // (two f16 powers by their exponent fields; a row that is not there has any)
+    const int field = static_cast<int>(exps[r + 8 * i]) - top + kRise + 15;
+    if ((there & 1u) != 0) least = min(least, field);
+    uint32_t f = static_cast<uint32_t>(max(field, 1)) * 0x04000400u;
+    if (clear && (there & 1u) == 0) {
       f = 0;
 #pragma unroll
       for (int half = 0; half < D / 64; ++half) x[half] = make_uint4(0, 0, 0, 0);
@@ -368,6 +379,21 @@ __device__ __forceinline__ void widen_tile(const uint8_t* src, const uint8_t* ex
       uint8_t* const line = out + half * 128 * 128;
       *reinterpret_cast<uint4*>(line + at0) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(line + at1) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  }
+  if (!__any_sync(0xffffffffu, least < 1)) return;  // (by warps: a branch by threads 2% slower)
+  out -= 4 * 8 * 128;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i, out += 8 * 128) {
+    const int e = static_cast<int>(exps[r + 8 * i]) - top + kRise + 14;
+    if (e >= 0) continue;
+    const float f1 = q8_power(max(e, -126));
+    const uint32_t f = pack_f16(f1, f1);
+#pragma unroll 1
+    for (int n = 0; n < D / 32; ++n) {
+      uint4* const at = reinterpret_cast<uint4*>(out + (n >> 1) * 128 * 128 + ((n & 1) ? at1 : at0));
+      const uint4 y = *at;
+      *at = make_uint4(mul_f16x2(y.x, f), mul_f16x2(y.y, f), mul_f16x2(y.z, f), mul_f16x2(y.w, f));
     }
   }
 }
@@ -847,7 +873,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.raw.q_ready);
-        const float scale = p.scale_log2 * q8_power(eq);
+        const float scale = p.scale_log2 * q8_power(-kRise) * q8_power(eq);
         int e_first = 127, e_values = 127;  // of V: the item's first tile, the last one seen
         for (int j = 0; j <= nkv && nkv > 0; ++j) {
           // step j: V of tile j - 1 and K of tile j, as everywhere
@@ -863,11 +889,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             }
             const uint32_t groups = *const_cast<volatile uint32_t*>(&sm.keys_ok[n % kOkRing]);
             const uint8_t* const exps = sm.raw.exps[n % Raw::kExps][0];
-            uint32_t live = 0;  // the thread's rows that are there
+            uint32_t there = 0;  // the thread's rows that are
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = widen_row<D>(t) + 8 * i;
-              if (kv == 0 || (((groups >> (row >> 4)) & 1u) != 0 && row < rows)) live |= 1u << i;
+              if (((groups >> (row >> 4)) & 1u) != 0 && row < rows) there |= 1u << i;
             }
             int top = e_values;
             if (kv == 0) {
@@ -880,10 +906,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
                 sm.raw.info[n % Raw::kInfos] =
                     TileInfo{fminf(fmaxf(scale * q8_scale(top), 1.17549435e-38f), 3.4e38f),
                              static_cast<float>(e_values - e_first + kShift),
-                             q8_power(e_first - 127 - kShift), 0.f};
+                             q8_power(e_first - 127 - kShift - kRise), 0.f};
             }
-            widen_tile<D>(kv == 0 ? sm.raw.k[slot] : sm.raw.v[slot], exps + kv * 128, top, live,
-                          kv == 0 ? sm.k[stage] : sm.v[stage], t);
+            widen_tile<D>(kv == 0 ? sm.raw.k[slot] : sm.raw.v[slot], exps + kv * 128, top, there,
+                          kv == 1, kv == 0 ? sm.k[stage] : sm.v[stage], t);
             __syncwarp();
             if (lane == 0) mbar_arrive(kv == 0 ? &sm.raw.k_empty[slot] : &sm.raw.v_empty[slot]);
             if (kv == 0) ++count; else ++values;
