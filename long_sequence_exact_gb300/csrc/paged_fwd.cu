@@ -144,6 +144,7 @@ struct RawTiles<D, true> {
   alignas(16) uint8_t exps[kExps][2][128];
   alignas(16) TileInfo info[kInfos];
   float top[4];      // largest |q| that the warps found
+  uint64_t q_top;    // all four are in `top`
   uint64_t q_ready;  // Q in f16
   uint64_t k_full[kRaw], k_empty[kRaw], v_full[kRaw], v_empty[kRaw];
 };
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       mbar_init(&sm.empty[s], 1);
     }
     if constexpr (Q8) {
+      mbar_init(&sm.raw.q_top, 4);
       mbar_init(&sm.raw.q_ready, 4);
       for (int i = 0; i < sm.raw.kRaw; ++i) {
         mbar_init(&sm.raw.k_full[i], 1 + 32);
@@ -852,8 +854,13 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           }
         }
         const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
-        if (lane == 0) sm.raw.top[warp - 12] = __uint_as_float(top << 16);
-        asm volatile("bar.sync 2, 128;" ::: "memory");
+        // (a wait with a limit, as all are here: a warp whose wait for the queries ran out has
+        // left, and does not come to a barrier)
+        if (lane == 0) {
+          sm.raw.top[warp - 12] = __uint_as_float(top << 16);
+          mbar_arrive(&sm.raw.q_top);
+        }
+        if (!take(&sm.raw.q_top, q_phase ^ 1)) break;
         const float most = fmaxf(fmaxf(sm.raw.top[0], sm.raw.top[1]),
                                  fmaxf(sm.raw.top[2], sm.raw.top[3]));
         int eq = static_cast<int>(__float_as_uint(most) >> 23) - 127 - 14;
