@@ -321,7 +321,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 //   rows to [2^14, 2^15): 8 bits are kept exactly down to 2^-29 of it.
 // - P is kept as f16, 11 bits.  The weights that are stored are 2^kShift of what the row
 //   sums count: below f16's normal range they are off by up to 2^-33 of the first tile's
-//   largest, times its largest |v|.  m starts at the first tile's maximum and moves where a
+//   largest, times its largest |v| (the first that has rows).  m starts at the first tile's maximum and moves where a
 //   weight would be stored as more than 2^15.  f32 results: a weight's remainder is a
 //   second f16.
 constexpr int kShift = 8;
@@ -399,7 +399,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* src, const uint8_t* ex
   }
 }
 
-// Largest exponent byte of a tile's rows that are there (127 where none is), by a warp.
+// Largest exponent byte of a tile's rows that are there (0 where none is), by a warp.
 __device__ __forceinline__ int top_exponent(const uint8_t* exps, uint32_t groups, int rows, int lane) {
   const uint32_t w = reinterpret_cast<const uint32_t*>(exps)[lane];
   uint32_t top = 0;
@@ -407,8 +407,7 @@ __device__ __forceinline__ int top_exponent(const uint8_t* exps, uint32_t groups
   for (int i = 0; i < 4; ++i)
     if (4 * lane + i < rows) top = max(top, (w >> (8 * i)) & 255u);
   if (((groups >> (lane >> 2)) & 1u) == 0) top = 0;
-  top = __reduce_max_sync(0xffffffffu, top);
-  return top > 0 ? static_cast<int>(top) : 127;
+  return static_cast<int>(__reduce_max_sync(0xffffffffu, top));
 }
 
 template <int D, bool kSplitP, bool Q8>
@@ -881,7 +880,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.raw.q_ready);
         const float scale = p.scale_log2 * q8_power(-kRise) * q8_power(eq);
-        int e_first = 127, e_values = 127;  // of V: the item's first tile, the last one seen
+        // of V: the item's first tile and the last one so far that have rows (weights of a
+        // tile without are 0, under any exponent)
+        int e_first = 127, e_values = 127;
+        bool none = true;
         for (int j = 0; j <= nkv && nkv > 0; ++j) {
           // step j: V of tile j - 1 and K of tile j, as everywhere
           if (!take(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
@@ -904,9 +906,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             }
             int top = e_values;
             if (kv == 0) {
-              top = top_exponent(exps, groups, rows, lane);
-              e_values = top_exponent(exps + 128, groups, rows, lane);
-              if (j == 0) e_first = e_values;
+              const int of_k = top_exponent(exps, groups, rows, lane);
+              const int of_v = top_exponent(exps + 128, groups, rows, lane);
+              top = of_k > 0 ? of_k : 127;
+              if (of_v > 0) {
+                e_values = of_v;
+                if (none) e_first = of_v;
+                none = false;
+              }
               if (t == 0)
                 // (a factor of 0 or infinity would make masked scores NaN; scores that the
                 // bounds change are 0 or infinite all the same)

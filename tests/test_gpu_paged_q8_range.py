@@ -27,6 +27,7 @@ FLOOR = {"decode": 0.0, "prefix": 2.0 ** -39, "few": 2.0 ** -39, "many": 0.0}
 
 def cache(k, v):
     """Rows k, v [n, D] in pages, scattered: (parts, table [1, pages], the rows as held)."""
+    k, v = (x.astype(np.float32).astype(np.float64) for x in (k, v))
     n, d = k.shape
     n_pages = -(-n // PAGE)
     order = np.random.default_rng(n).permutation(n_pages + 2)[:n_pages]
@@ -147,3 +148,32 @@ def test_small_keys_beside_a_large_one(form, apart, d, out_dtype):
     vmax = np.abs(vh).max()
     floor = (2.0 ** -35 if form == "decode" else FLOOR[form]) * vmax
     check(form, out_dtype, (o, lse), want, error + lost, floor)
+
+
+# ------------------------------------------------------ pages that do not exist
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [-39, -100, -8, 7])
+@pytest.mark.parametrize("gone", [range(0, 8), range(1, 24), range(8, 16)], ids=["first", "behind", "second"])
+@pytest.mark.parametrize("form", FORMS)
+def test_small_values_behind_missing_pages(form, gone, size, d, out_dtype):
+    """Values of any size behind 128 keys or more without pages, which are left out: the
+    weights keep their bits whatever stands in for the missing tiles."""
+    r = np.random.default_rng(200 + size)
+    n = 430
+    k, v = r.standard_normal((n, d)), r.uniform(0.2, 1.0, (n, d)) * 448 * 2.0 ** size
+    v[:, 3] = 448 * 2.0 ** size
+    q = r.standard_normal(d)
+    q = f64(torch.from_numpy(q).to(BF16))
+    scale = 0.125
+    parts, table, (kh, vh) = cache(k, v)
+    ok = np.ones(n, bool)
+    for i, g in enumerate(gone):
+        table[0, g] = (-1, 1 << 20)[i % 2]
+        ok[g * PAGE:(g + 1) * PAGE] = False
+    o, lse, last = call(form, parts, table, n, q, scale, out_dtype)
+    assert done() == -10
+    want = exact(kh, vh, q, scale, last, ok)
+    error = 2 * (d + 2) * P.U32 * scale * np.linalg.norm(q) * np.linalg.norm(kh, axis=-1).max()
+    # a weight is off by no more than 2^-32 of the largest value (decode 2^-35), as is V
+    check(form, out_dtype, (o, lse), want, error, (2.0 ** -32 + FLOOR[form]) * np.abs(vh).max())
