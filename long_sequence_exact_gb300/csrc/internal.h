@@ -26,7 +26,7 @@ enum KernelId {
   kKidFwdTc = 0, kKidDkdv, kKidDq, kKidRowDot, kKidMerge, kKidTreeMerge,
   kKidDecode, kKidSimtFwd, kKidSimtBwd, kKidFill, kKidTranspose, kKidBlockLists,
   kKidBwdFused, kKidDqConvert, kKidPageMap, kKidPageAppend, kKidPagedDecode, kKidPagedMerge,
-  kKidPagedFwd, kKidPagedPlan, kKidPageRead, kKidCount
+  kKidPagedFwd, kKidPagedPlan, kKidPageRead, kKidPageWiden, kKidCount
 };
 
 // Sequence-contiguous copies (layout.cu): a bf16 [B, H, N, D] view is

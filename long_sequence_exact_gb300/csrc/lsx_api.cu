@@ -41,7 +41,7 @@ const char* const kKernelNames[kKidCount] = {
     "fwd_tc", "bwd_dkdv_tc", "bwd_dq_tc", "bwd_row_dot", "merge", "tree_merge",
     "decode_partials", "simt_fwd", "simt_bwd", "fill", "transpose", "block_lists",
     "bwd_fused_tc", "bwd_dq_convert", "page_map", "page_append", "paged_decode", "paged_merge",
-    "paged_fwd", "paged_plan", "page_read"};
+    "paged_fwd", "paged_plan", "page_read", "page_widen"};
 std::atomic<bool> g_timing{false};
 struct TimedLaunch {
   int kid;

@@ -379,9 +379,9 @@ int launch_page_widen(const PagedCache8& c, const int32_t* kv_lens, const int32_
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  timing_begin(kKidPageRead, s);
+  timing_begin(kKidPageWiden, s);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, page_widen_kernel, p);
-  timing_end(kKidPageRead, s);
+  timing_end(kKidPageWiden, s);
   return e == cudaSuccess ? LSX_OK : LSX_ERR_LAUNCH;
 }
 
