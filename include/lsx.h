@@ -476,6 +476,11 @@ int attn_paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_ten
  *     computed from a bf16 copy of the pages that they see, in the workspace: 4 GiB at
  *     most (a larger one is not made, and the call works as with few rows).  They round P
  *     to bf16 for a bf16 o, as attn_paged_fwd does, and keep 16 bits for an f32 one.
+ *   The copy is the caller's choice: its room follows from the pool and the table's width,
+ *   not from what is in them, and attn_paged_fwd_q8_workspace_size names it with the rest
+ *   (so that fewer sequences or a narrower table, which bring the copy in, can need more).
+ *   With a smaller workspace, down to what attn_paged_fwd_workspace_size names for the same
+ *   sizes, the call works without the copy, as with few rows.
  * ---------------------------------------------------------------------- */
 int attn_page_append_q8(const lsx_tensor* k, const lsx_tensor* v, const int64_t* slot_map,
                         const lsx_tensor* k_pages, const lsx_tensor* k_scales,

@@ -145,12 +145,13 @@ int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tens
                   const PrefixPlan& plan,
                   float scale, bool split_p, float* part_o, float* part_l,
                   const DeviceCtx& ctx, cudaStream_t s);
-// Ragged prompt tokens, causal, over the pages.
+// Ragged prompt tokens, causal, over the pages.  copy: with a bf16 copy of an 8-bit cache,
+// where the sizes are for one; the call goes without where the workspace has no room for it.
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
-                           int64_t max_pages, bool q8, int sm_count);
+                           int64_t max_pages, bool copy, int sm_count);
 int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                      const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
                      const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse,
-                     void* workspace, const DeviceCtx& ctx, cudaStream_t s);
+                     void* workspace, size_t workspace_bytes, const DeviceCtx& ctx, cudaStream_t s);
 
 }  // namespace lsx

@@ -315,13 +315,13 @@ int attn_paged_decode_q8(const lsx_tensor* q, const lsx_tensor* k_pages,
 
 // (a refused size: 0; the call itself says why)
 static size_t fwd_workspace(const lsx_tensor* q, const lsx_tensor* k_pages, int64_t batch,
-                            int64_t max_pages, bool q8) {
+                            int64_t max_pages, bool copy) {
   if (q == nullptr || k_pages == nullptr || check_page_sizes(*k_pages) != LSX_OK ||
       check_query_sizes(*q, *k_pages) != LSX_OK ||
       check_prompt_sizes(*q, *k_pages, batch) != LSX_OK ||
       check_table_size(max_pages, k_pages->N) != LSX_OK)
     return 0;
-  return paged_fwd_workspace(*q, *k_pages, batch, max_pages, q8, sm_count_or(kSmFallback));
+  return paged_fwd_workspace(*q, *k_pages, batch, max_pages, copy, sm_count_or(kSmFallback));
 }
 
 size_t attn_paged_fwd_workspace_size(const lsx_tensor* q, const lsx_tensor* k_pages,
@@ -341,16 +341,16 @@ static int paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_t
   LSX_TRY(check_ints(kv_lens));
   LSX_TRY(check_ints(cu_q));
   if (q->N == 0) return LSX_OK;
-  LSX_TRY(check_ws(workspace, workspace_bytes,
-                   fwd_workspace(q, k_pages, batch, max_pages, pages8 != nullptr)));
+  // (8 bits: the copy's room is not asked for)
+  LSX_TRY(check_ws(workspace, workspace_bytes, fwd_workspace(q, k_pages, batch, max_pages, false)));
   DeviceCtx ctx;
   LSX_TRY(device_ctx(&ctx));
   const PagedCache c = paged_cache(*k_pages, *v_pages, block_table, table_stride, max_pages);
   PagedCache8 c8;
   if (pages8 != nullptr) c8 = paged_cache8(*pages8, block_table, table_stride, max_pages);
   return launch_paged_fwd(*q, *k_pages, *v_pages, c, pages8 != nullptr ? &c8 : nullptr, kv_lens,
-                          cu_q, batch, resolve_scale(scale, q->D), *o, *lse, workspace, ctx,
-                          as_stream(stream));
+                          cu_q, batch, resolve_scale(scale, q->D), *o, *lse, workspace,
+                          workspace_bytes, ctx, as_stream(stream));
 }
 
 int attn_paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_tensor* v_pages,

@@ -1638,7 +1638,7 @@ int64_t dense_pages(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, in
   return bytes <= kMostDense && q.N * (q.H / kp.H) >= dense_rows(q.D) * batch ? pages : 0;
 }
 FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, int64_t max_pages,
-                     bool q8, int sm_count) {
+                     bool copy, int sm_count) {
   FwdLayout x;
   const int64_t G = q.H / kp.H, tpt = G <= 128 ? 128 / G : 1;
   const int64_t tiles = ceil_div(max_pages * kp.N, 128);
@@ -1651,12 +1651,12 @@ FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, i
   const size_t rows = static_cast<size_t>(x.max_slots * kp.H) * 256;
   x.part_o = x.part_l + align256(rows * 4);
   x.dense_table = x.part_o + align256(rows * static_cast<size_t>(q.D) * 4);
-  x.dense_pages = q8 ? dense_pages(q, kp, batch, max_pages) : 0;
-  const size_t copy = align256(static_cast<size_t>(x.dense_pages * kp.N * kp.H * kp.D) * 2);
+  x.dense_pages = copy ? dense_pages(q, kp, batch, max_pages) : 0;
+  const size_t dense = align256(static_cast<size_t>(x.dense_pages * kp.N * kp.H * kp.D) * 2);
   x.dense_k = x.dense_table +
               (x.dense_pages > 0 ? align256(static_cast<size_t>(batch * max_pages) * 4) : 0);
-  x.dense_v = x.dense_k + copy;
-  x.total = x.dense_v + copy;
+  x.dense_v = x.dense_k + dense;
+  x.total = x.dense_v + dense;
   return x;
 }
 
@@ -1725,16 +1725,19 @@ int launch_prefix(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tens
 }
 
 size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64_t batch,
-                           int64_t max_pages, bool q8, int sm_count) {
-  return fwd_layout(q, k_pages, batch, max_pages, q8, sm_count).total;
+                           int64_t max_pages, bool copy, int sm_count) {
+  return fwd_layout(q, k_pages, batch, max_pages, copy, sm_count).total;
 }
 
 int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& pages_k, const lsx_tensor& pages_v,
                      const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
                      const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse,
-                     void* workspace, const DeviceCtx& ctx, cudaStream_t s) {
+                     void* workspace, size_t workspace_bytes, const DeviceCtx& ctx,
+                     cudaStream_t s) {
   const bool split_p = c8 != nullptr && o.dtype == LSX_F32;
-  const FwdLayout x = fwd_layout(q, pages_k, batch, c.max_pages, c8 != nullptr, ctx.sm_count);
+  FwdLayout x = fwd_layout(q, pages_k, batch, c.max_pages, c8 != nullptr, ctx.sm_count);
+  if (workspace_bytes < x.total)  // no room for the copy: the caller goes without
+    x = fwd_layout(q, pages_k, batch, c.max_pages, false, ctx.sm_count);
   char* ws = static_cast<char*>(workspace);
   FwdParams p;
   p.c = c;

@@ -323,7 +323,9 @@ def paged_fwd_q8(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, 
                  out=None, lse=None, workspace=None, out_dtype=None):
     """paged_fwd over an 8-bit cache: attention over the numbers that it stands for.
     Where the sequences have 8 D query rows of a kv head on the average, or more, a
-    bf16 copy of the pages that they see is made in the workspace, up to 4 GiB.
+    bf16 copy of the pages that they see is made in the workspace, up to 4 GiB (its room
+    follows from the pool and the table's width).  With a workspace of
+    paged_fwd_q8_workspace_size(..., copy=False) bytes the call goes without the copy.
     Returns (O, LSE) of the packed tokens."""
     lib = _lib._lib or load()
     dev = _device(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_q, out, lse,
@@ -342,6 +344,10 @@ def paged_fwd_q8(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, 
     return out, lse
 
 
-def paged_fwd_q8_workspace_size(q, k_pages, batch, max_pages) -> int:
+def paged_fwd_q8_workspace_size(q, k_pages, batch, max_pages, copy=True) -> int:
+    """Bytes with room for the bf16 copy, where the sizes are for one, or (copy=False)
+    without, which is enough.  A size that includes a copy can exceed that of more
+    sequences or a wider table; one without it does not."""
     vq, kp = _pack(q, k_pages, kinds=_KINDS8)
-    return int(load().attn_paged_fwd_q8_workspace_size(vq, kp, int(batch), int(max_pages)))
+    size = load().attn_paged_fwd_q8_workspace_size if copy else load().attn_paged_fwd_workspace_size
+    return int(size(vq, kp, int(batch), int(max_pages)))

@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import long_sequence_exact_gb300 as lsx
+import paged_ref as P
 from long_sequence_exact_gb300 import _lib
-from test_gpu_paged import done, ints
+from test_gpu_paged import check_prompt, done, ints
 from test_gpu_paged_q8_attention import prompt_case
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +39,29 @@ def test_the_copy_is_timed_as_itself():
     got = kernels(lambda: lsx.page_read_q8(*c.parts, table[:1], ints([0]), ints([0, n]), n))
     assert got == {"page_read": 1}
     assert done() == 0
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompts_of_many_rows_without_room_for_a_copy(d, out_dtype):
+    """The workspace decides: with room for the copy it is made, with a byte less, or with
+    the size without it, the tiles are widened where they are used, bit for bit alike; NaN
+    behind the workspace's end is not read, and stays."""
+    q, c, table, lens, cu = prompt_case(8, 2, d, 32, [(700, 300), (0, 300)], tail=3)
+    dense = c.dense()
+    o_ref, l_ref = P.fwd(q, *dense, table, lens, cu)
+    full, rest = (lsx.paged_fwd_q8_workspace_size(q, c.kp, 2, table.shape[1], copy=x) for x in (True, False))
+    assert full > rest > 0
+    outs = []
+    for n in (full, full - 1, rest):
+        ws = torch.full((full + 512,), 255, dtype=torch.uint8, device=DEV)
+        ws = ws[(-ws.data_ptr()) % 256:]
+        o, lse = torch.full(q.shape, 7.0, dtype=out_dtype, device=DEV), torch.full(q.shape[:3], 7.0, device=DEV)
+        got = kernels(lambda: lsx.paged_fwd_q8(q, *c.parts, table, ints(lens), ints(cu), out=o, lse=lse, workspace=ws[:n]))
+        assert ("page_widen" in got) == (n == full) and done() == 0
+        assert bool((ws[n:] == 255).all())
+        bits = ((2.0 ** -8, 2.0 ** -16) if n == full else (2.0 ** -11, 2.0 ** -22))[out_dtype is torch.float32]
+        tol, tol_lse = P.tolerances(q, *dense, bits, out_dtype)
+        check_prompt(o, lse, o_ref, l_ref, tol, tol_lse)
+        outs.append((o, lse))
+    assert all(torch.equal(a, b) for a, b in zip(outs[1], outs[2]))
