@@ -1622,20 +1622,32 @@ struct FwdLayout {
 };
 
 // Prompts over an 8-bit cache read a bf16 copy of the pages that they see (paged_q8.cu),
-// where the copy (with its table) has at most kMostDense bytes and the sequences
-// dense_rows each for a key head, or more, on the average; otherwise the tiles are
-// widened where they are used.  One sequence after 32768 keys, 32 query heads over 8 of
-// 128, rows: by a copy, in place, us: 256: 95, 67; 512: 116, 99; 1024: 173, 171; 2048:
-// 265, 290; 4096: 439, 583.  Eight after 8192 keys each: 264: 101, 83; 529: 138, 126; 1060:
-// 175, 181; 2123: 269, 300.  Heads of 64, one: 512: 83, 87; 1024: 130, 149; 2048: 210, 249;
-// eight: 529: 103, 106; 1060: 135, 161.
+// where the copy (with its table) has at most kMostDense bytes and the sequences more than
+// dense_rows each for a key head, on the average; otherwise the tiles are widened where they
+// are used, which keeps more bits of P.  32 query heads over 8, bf16 results, by a copy and
+// in place, us:
+//   rows                       1024        1280        1536        2048        4096
+//   128, after 8192 keys     71   67     77   79     83   81     98  104    143  169
+//   128, after 32768        169  161    194  192    196  205    261  282    435  537
+//   128, after 65536        284  274    335  337    348  368    450  495    822 1023
+//   128, 8 x after 8192     300  294                409  429    521  568
+//   rows                        512        1024        1280        2048        4096
+//   64, after 8192           44   42     56   59     63   69     81   91    118  149
+//   64, after 32768          86   79    132  138    151  165    212  241    368  482
+//   64, after 65536         134  130    218  239    259  290    358  431    690  926
+// f32 results cross later, since the copy's second product of P costs more beside less
+// else: of 128 at 1500 to 2000 rows (after 32768 keys 1024 rows 261 and 233, 2048 421 and
+// 409, 4096 675 and 806), of 64 at 2000 to 4000 (2048 rows 384 and 333, 4096 652 and 689).
+// The border is one for both, since workspaces are asked for without the results' type.  One
+// long prompt beside 15 single tokens after 4000 keys, whose pages are copied as well:
+// 210 both ways, of 64 101.
 constexpr double kMostDense = 4294967296.0;
 constexpr int64_t dense_rows(int64_t d) { return 8 * d; }
 int64_t dense_pages(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, int64_t max_pages) {
   const int64_t pages = batch * max_pages < kp.B ? batch * max_pages : kp.B;
   const double bytes = 4.0 * (static_cast<double>(pages) * static_cast<double>(kp.N * kp.H * kp.D) +
                               static_cast<double>(batch * max_pages));
-  return bytes <= kMostDense && q.N * (q.H / kp.H) >= dense_rows(q.D) * batch ? pages : 0;
+  return bytes <= kMostDense && q.N * (q.H / kp.H) > dense_rows(q.D) * batch ? pages : 0;
 }
 FwdLayout fwd_layout(const lsx_tensor& q, const lsx_tensor& kp, int64_t batch, int64_t max_pages,
                      bool copy, int sm_count) {

@@ -322,7 +322,7 @@ def paged_decode_q8_workspace_size(q, k_pages, max_pages, prefix_len=0) -> int:
 def paged_fwd_q8(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_q, scale=None,
                  out=None, lse=None, workspace=None, out_dtype=None):
     """paged_fwd over an 8-bit cache: attention over the numbers that it stands for.
-    Where the sequences have 8 D query rows of a kv head on the average, or more, a
+    Where the sequences have more than 8 D query rows of a kv head on the average, a
     bf16 copy of the pages that they see is made in the workspace, up to 4 GiB (its room
     follows from the pool and the table's width).  With a workspace of
     paged_fwd_q8_workspace_size(..., copy=False) bytes the call goes without the copy.

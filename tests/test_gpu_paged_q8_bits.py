@@ -70,7 +70,7 @@ def sized_case(d, keys, order, span, form):
     given, with scores that make up for them: weights 2^-e, values 2^e."""
     n, page, hkv = 700, 16, 2
     b = 17 if form == "prefix" else 1
-    new = {"few": 3, "many": 8 * d // 4}.get(form, 1)
+    new = {"few": 3, "many": 8 * d // 4 + 1}.get(form, 1)
     q, c, table, prefix = decode_case(8, hkv, 1, d, page, [n], 0, seed=170, width=keys // page, spread=0)
     e = np.round(span * ORDERS[order](np.arange(n) / (n - 1.0))).astype(int)
     pos = np.arange(n)

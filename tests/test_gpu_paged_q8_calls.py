@@ -13,7 +13,7 @@ from test_gpu_paged_q8_attention import prompt_case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-MANY = (8, 2, 64, 32, [(700, 300), (0, 200)])   # 8 D rows a sequence and key head and more: by a copy
+MANY = (8, 2, 64, 32, [(700, 300), (0, 200)])   # more than 8 D rows a sequence and key head: by a copy
 
 
 def kernels(fn):
@@ -65,3 +65,22 @@ def test_prompts_of_many_rows_without_room_for_a_copy(d, out_dtype):
         check_prompt(o, lse, o_ref, l_ref, tol, tol_lse)
         outs.append((o, lse))
     assert all(torch.equal(a, b) for a, b in zip(outs[1], outs[2]))
+
+
+@pytest.mark.parametrize("width", [0, 400])
+@pytest.mark.parametrize("tokens", [256, 257])
+def test_the_border_of_the_copy(tokens, width):
+    """As many rows as 8 D a sequence are worked on in place, which is faster there and
+    keeps P to f16; one token more by a copy, whose pages are numbered by sequence and
+    column or, behind a wide table, as in the pool."""
+    q, c, table, lens, cu = prompt_case(32, 8, 128, 64, [(3000, tokens)])
+    if width:
+        table = torch.cat([table, torch.full((1, width), -1, dtype=torch.int32, device=DEV)], 1)
+        assert table.shape[1] > c.kp.shape[0]
+    dense = c.dense()
+    o_ref, l_ref = P.fwd(q, *dense, table, lens, cu)
+    out = []
+    got = kernels(lambda: out.extend(lsx.paged_fwd_q8(q, *c.parts, table, ints(lens), ints(cu))))
+    assert ("page_widen" in got) == (tokens > 256) and done() == 0
+    tol, tol_lse = P.tolerances(q, *dense, 2.0 ** -8 if tokens > 256 else 2.0 ** -11, torch.bfloat16)
+    check_prompt(*out, o_ref, l_ref, tol, tol_lse)

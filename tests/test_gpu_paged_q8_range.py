@@ -52,7 +52,7 @@ def call(form, parts, table, n, q, scale, out_dtype):
                                      table[0], n, out_dtype=out_dtype)
         last = np.full((17, G, 1), n - 1)
     else:
-        new = 3 if form == "few" else 8 * d // G
+        new = 3 if form == "few" else 8 * d // G + 1
         o, lse = lsx.paged_fwd_q8(q.expand(1, G, new, d).contiguous(), *parts, table, ints([n]), ints([0, new]),
                                   scale, out_dtype=out_dtype)
         last = np.broadcast_to(n - new + np.arange(new), (G, new))

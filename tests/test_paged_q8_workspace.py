@@ -17,6 +17,12 @@ def test_the_copy_is_named(lib):  # noqa: F811
     rows = 2 * 40 * 16                                         # of the pages that two tables name
     assert copy - rest == 2 * rows * 2 * 128 * 2 + 512         # and the table of 80 entries, 256 bytes each way
     assert sizes(lib, _t(b=1, h=8, n=500), 2, 40)[0] == sizes(lib, _t(b=1, h=8, n=500), 2, 40)[1]
+    # more than 8 D rows a sequence: 256 tokens of four heads are as many
+    for d in (64, 128):
+        for n, more in ((2 * d, False), (2 * d + 1, True)):
+            copy, rest = (f(R(_t(b=1, h=8, n=n, d=d)), R(pages(p=400, d=d)), 1, 40)
+                          for f in (lib.attn_paged_fwd_q8_workspace_size, lib.attn_paged_fwd_workspace_size))
+            assert (copy > rest) == more
     # sizes without a copy grow with the batch and the width; those with one need not
     for q in (MANY["q"], _t(b=1, h=8, n=40)):
         rest = [[sizes(lib, q, b, w)[1] for w in (4, 40, 400, 4000)] for b in (1, 2, 3, 8, 64)]
