@@ -471,7 +471,7 @@ int attn_paged_fwd(const lsx_tensor* q, const lsx_tensor* k_pages, const lsx_ten
  *     kv head share (heads of 64: 64), keep P to the same bits, and no weight better than
  *     to 2^-32 of the largest |v|; an element of q to 2^-39 of the largest one among the
  *     rows that are worked on together (up to 256 of one kv head), one of k or v to
- *     2^-39 of the largest in 128 neighbouring keys.
+ *     2^-39 of the largest in 128 neighbouring keys (v: or 2^-100 of the largest |v|).
  *   - Prompts with more than 8 D query rows of a kv head a sequence, on the average, are
  *     computed from a bf16 copy of the pages that they see, in the workspace: 4 GiB at
  *     most (a larger one is not made, and the call works as with few rows).  They round P

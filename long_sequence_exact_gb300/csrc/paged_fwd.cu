@@ -128,9 +128,10 @@ struct Cfg {
 // softmax needs of each tile.
 struct TileInfo {
   float factor;  // of its scores
-  float shift;   // its weights are 2^shift of what the row sums count
-  float unit;    // what O is in units of (the same for all tiles of an item)
-  float pad;
+  float shift;   // its weights are 2^shift of what the row sums count; NaN: kShift, and
+                 // O's unit is another than before
+  float unit;    // what O is in units of
+  float grow;    // the unit before in terms of it
 };
 template <int D, bool Q8>
 struct RawTiles {};
@@ -319,13 +320,20 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 //   all its weights.
 // - Q becomes f16 times a power of two that brings the largest element of an item's
 //   rows to [2^14, 2^15): 8 bits are kept exactly down to 2^-29 of it.
-// - P is kept as f16, 11 bits.  The weights that are stored are 2^kShift of what the row
-//   sums count: below f16's normal range they are off by up to 2^-33 of the first tile's
-//   largest, times its largest |v| (the first that has rows).  m starts at the first tile's maximum and moves where a
-//   weight would be stored as more than 2^15.  f32 results: a weight's remainder is a
-//   second f16.
+// - P is kept as f16, 11 bits.  The weights that are stored are 2^(kShift + E - E_ref) of
+//   what the row sums count, E_ref the exponent of O's unit: below f16's normal range they
+//   are off by up to 2^-33 of the row's largest, times 448 2^E_ref.  E_ref is the first
+//   tile's E (that has rows), and a later one's where it is above that by more than kSlack:
+//   O is then divided by as much, and the row sums stay as they are (with one unit for an
+//   item, m had to make up for it: sums and LSE lost bits where values grew by 2^100).  An E
+//   further than kFar below E_ref counts as that much, so that the sums, taken of the
+//   weights as they are stored before they are f16, stay in range.  m starts at the first
+//   tile's maximum and moves where a weight would be stored as more than 2^15.  f32
+//   results: a weight's remainder is a second f16.
 constexpr int kShift = 8;
 constexpr int kRise = 7;
+constexpr int kSlack = 6;
+constexpr int kFar = 64;
 
 // A tile [128][D] of e4m3 (rows of 128 bytes with the 128-byte swizzle, of 64 without)
 // to the f16 tile that the products read; thread t of 128.  `there`: a bit for each of the
@@ -880,9 +888,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.raw.q_ready);
         const float scale = p.scale_log2 * q8_power(-kRise) * q8_power(eq);
-        // of V: the item's first tile and the last one so far that have rows (weights of a
-        // tile without are 0, under any exponent)
-        int e_first = 127, e_values = 127;
+        // of O's unit and of V's tile (weights of a tile without rows are 0 under any exponent)
+        int e_ref = 127, e_values = 127;
         bool none = true;
         for (int j = 0; j <= nkv && nkv > 0; ++j) {
           // step j: V of tile j - 1 and K of tile j, as everywhere
@@ -909,18 +916,21 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
               const int of_k = top_exponent(exps, groups, rows, lane);
               const int of_v = top_exponent(exps + 128, groups, rows, lane);
               top = of_k > 0 ? of_k : 127;
-              if (of_v > 0) {
-                e_values = of_v;
-                if (none) e_first = of_v;
+              float shift = __uint_as_float(0x7fffffffu), grow = 1.f;
+              if (of_v > (none ? 0 : e_ref + kSlack)) {
+                grow = none ? 1.f : q8_power(e_ref - of_v);
+                e_ref = e_values = of_v;
                 none = false;
+              } else {
+                if (of_v > 0) e_values = max(of_v, e_ref - kFar);
+                shift = static_cast<float>(e_values - e_ref + kShift);
               }
               if (t == 0)
                 // (a factor of 0 or infinity would make masked scores NaN; scores that the
                 // bounds change are 0 or infinite all the same)
                 sm.raw.info[n % Raw::kInfos] =
                     TileInfo{fminf(fmaxf(scale * q8_scale(top), 1.17549435e-38f), 3.4e38f),
-                             static_cast<float>(e_values - e_first + kShift),
-                             q8_power(e_first - 127 - kShift - kRise), 0.f};
+                             shift, q8_power(e_ref - 127 - kShift - kRise), grow};
             }
             widen_tile<D>(kv == 0 ? sm.raw.k[slot] : sm.raw.v[slot], exps + kv * 128, top, there,
                           kv == 1, kv == 0 ? sm.k[stage] : sm.v[stage], t);
@@ -972,8 +982,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         s_phase ^= 1;
         tc_fence_after();
         const uint32_t okm = *const_cast<volatile uint32_t*>(&sm.keys_ok[tile % kOkRing]);
-        // O_t under a new reference; it must hold the finished P_t V of the tile before
-        auto rescale = [&](float m_new) {
+        // O_t under a new reference, and times `unit_by`; it must hold the finished P_t V of
+        // the tile before
+        auto rescale = [&](float m_new, float unit_by) {
           if (!wait(&sm.o_full[t], s_phase)) return false;
           tc_fence_after();
           const float alpha = l > 0.f ? ex2(m - m_new) : 0.f;
@@ -984,7 +995,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             tmem_ld_wait32(u);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+              u[i] = __float_as_uint(__uint_as_float(u[i]) * (alpha * unit_by));
             tmem_st32(tO + cc * 32, u);
           }
           tmem_st_wait();
@@ -993,7 +1004,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         };
         if constexpr (Q8) {
           const TileInfo& info = sm.raw.info[tile % RawTiles<D, true>::kInfos];
-          const float f = info.factor, shift = info.shift;
+          const float f = info.factor;
+          float shift = info.shift;
           unit = info.unit;
           // The maximum first, 32 scores at a time; masked ones are written back.  (In short
           // loops: see the instruction cache above.)
@@ -1021,11 +1033,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           tmem_st_wait();
           // m moves where a weight that is stored would pass 2^15, and for a row's first keys
           const float top = mx * f;
-          if (__any_sync(0xffffffffu, live && top > kNegInf && !(l > 0.f && top - m + shift <= 15.f))) {
+          if (__any_sync(0xffffffffu, live && !(l > 0.f && top - m + shift <= 15.f))) {
+            if (!(shift < 1000.f)) shift = kShift;
             float m_new = fmaxf(top, top + (shift - 8.f));
             m_new = l > 0.f ? fmaxf(m, m_new) : m_new;
             if (!(m_new > kNegInf)) m_new = m;
-            if (!first && !rescale(m_new)) { ok = false; break; }
+            if (!first && !rescale(m_new, info.grow)) { ok = false; break; }
             m = m_new;
           }
           const float nm = shift - m;
@@ -1167,7 +1180,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           // the weights stored first have landed before others follow them
           tmem_st_wait();
           if (!first) {
-            if (!rescale(m_new)) { ok = false; break; }
+            if (!rescale(m_new, 1.f)) { ok = false; break; }
           }
           m = m_new;
           part = weights();

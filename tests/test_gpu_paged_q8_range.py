@@ -25,7 +25,7 @@ P_BITS = {"decode": (2.0 ** -11, 2.0 ** -22), "prefix": (2.0 ** -11, 2.0 ** -22)
 FLOOR = {"decode": 0.0, "prefix": 2.0 ** -39, "few": 2.0 ** -39, "many": 0.0}
 
 
-def cache(k, v):
+def cache(k, v, held=True):
     """Rows k, v [n, D] in pages, scattered: (parts, table [1, pages], the rows as held)."""
     k, v = (x.astype(np.float32).astype(np.float64) for x in (k, v))
     n, d = k.shape
@@ -35,7 +35,7 @@ def cache(k, v):
     slots = [int(order[i // PAGE]) * PAGE + i % PAGE for i in range(n)]
     rows = [torch.from_numpy(x).to(DEV, F32)[None, None] for x in (k, v)]
     lsx.page_append_q8(*rows, kp, ks, vp, vs, ints(slots, torch.int64))
-    return (kp, ks, vp, vs), ints(order[None].copy()), [Q.values(*Q.codes(x)) for x in (k, v)]
+    return (kp, ks, vp, vs), ints(order[None].copy()), [Q.values(*Q.codes(x)) if held else None for x in (k, v)]
 
 
 def call(form, parts, table, n, q, scale, out_dtype):
@@ -177,3 +177,67 @@ def test_small_values_behind_missing_pages(form, gone, size, d, out_dtype):
     error = 2 * (d + 2) * P.U32 * scale * np.linalg.norm(q) * np.linalg.norm(kh, axis=-1).max()
     # a weight is off by no more than 2^-32 of the largest value (decode 2^-35), as is V
     check(form, out_dtype, (o, lse), want, error, (2.0 ** -32 + FLOOR[form]) * np.abs(vh).max())
+
+
+# ------------------------------------------------------------- values of zero
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("order", ["behind", "before", "between"])
+@pytest.mark.parametrize("large", [57344.0, 1.0, 448 * 2.0 ** -100])
+@pytest.mark.parametrize("form", FORMS + ["whole"])
+def test_many_keys_of_value_zero(form, large, order, out_dtype):
+    """2^17 keys of value 0 and 2^-28 of the weight of one key of a large value (57344: e4m3
+    at the end of the exponents' range): they count in the row sums, 2^-11 of them, whatever
+    the exponents of their values are.  "whole": a prefix under so many rows that it is not
+    cut into pieces, with sums of their own."""
+    n, d = (1 << 17) + 384, 64
+    k, v = np.zeros((n, d)), np.zeros((n, d))
+    k[:, 0] = -28.0
+    at = {"behind": 5, "before": n - 200, "between": n // 2 + 7}[order]
+    k[at, 0] = 0.0
+    v[at] = large
+    v[at, 1::2] = -large
+    q = np.zeros(d)
+    q[0] = 1.0
+    scale = float(np.float32(np.log(2)))
+    parts, table, _ = cache(k, v, False)
+    if form == "whole":
+        b = 2 * 152 * 256 // G
+        o, lse = lsx.paged_decode_q8(torch.from_numpy(q).to(DEV, BF16).expand(b, G, 1, d).contiguous(), *parts,
+                                     torch.full((b, 1), -1, dtype=torch.int32, device=DEV),
+                                     torch.zeros(b, dtype=torch.int32, device=DEV), scale, table[0], n,
+                                     out_dtype=out_dtype)
+        assert bool((o == o[:1, :1]).all()) and bool((lse == lse[0, 0]).all())
+        o, lse, last = f64(o[0, :1, 0]), f64(lse[0, :1, 0]), np.array([n - 1])
+    else:
+        o, lse, last = call(form, parts, table, n, q, scale, out_dtype)
+    assert done() == 0
+    # (a row's result is that of the key at `at` times its weight)
+    seen = last + 1
+    total = 1.0 + (seen - 1) * np.exp(-28.0 * scale)
+    want = Q.values(*Q.codes(v[at:at + 1])) / total[:, None]
+    # arguments in log2 below 2^5, the exponential, sums; P's own rounding is none (2^0)
+    rel = 32 * P.U32 + 2.0 ** -21 + 2.0 ** -19
+    assert (np.abs(lse - np.log(total)) <= rel + 2 * P.U32).all()
+    lim = rel + 2.0 ** -21 + (P.U16 if out_dtype is BF16 else 0.0)
+    assert (np.abs(o - want) <= lim * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_first_keys_of_value_zero(form, d):
+    """Values of 0 in the first tiles, as of padding, and of ordinary size behind: LSE and
+    results are as near as with ordinary values throughout."""
+    r = np.random.default_rng(300 + d)
+    n = 700
+    k, v = r.standard_normal((n, d)), r.standard_normal((n, d))
+    v[:260] = 0.0
+    v[420:560] = 0.0
+    q = f64(torch.from_numpy(r.standard_normal(d)).to(BF16))
+    scale = 0.125
+    parts, table, (kh, vh) = cache(k, v)
+    error = 2 * (d + 2) * P.U32 * scale * np.linalg.norm(q) * np.linalg.norm(kh, axis=-1).max()
+    for out_dtype in (BF16, F32):
+        o, lse, last = call(form, parts, table, n, q, scale, out_dtype)
+        assert done() == 0
+        want = exact(kh, vh, q, scale, last)
+        check(form, out_dtype, (o, lse), want, error, (2.0 ** -32 + FLOOR[form]) * np.abs(vh).max())
