@@ -128,7 +128,8 @@ size_t paged_decode_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, in
                               int64_t prefix_len, bool q8, int sm_count);
 int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                         const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
-                        const int32_t* prefix_table, int64_t prefix_len, float scale, const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
+                        const int32_t* prefix_table, int64_t prefix_len, float scale,
+                        const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
                         const DeviceCtx& ctx, cudaStream_t s);
 // Partials of every decode query against a prefix that all of them see, on
 // the prompt kernel: piece i of the row that is token (b, n) of head g of kv head
@@ -151,7 +152,8 @@ size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64
                            int64_t max_pages, bool copy, int sm_count);
 int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                      const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
-                     const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse,
-                     void* workspace, size_t workspace_bytes, const DeviceCtx& ctx, cudaStream_t s);
+                     const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o,
+                     const lsx_tensor& lse, void* workspace, size_t workspace_bytes,
+                     const DeviceCtx& ctx, cudaStream_t s);
 
 }  // namespace lsx

@@ -599,9 +599,9 @@ static_assert(2 * (kSmem<128> + 1024) <= 228 * 1024, "shared memory of two CTAs"
 
 // Units a cluster each: all of them on the device at once, and short (the
 // table's width bounds the keys; the lengths are not known here, so that a short
-// sequence behind a wide table takes runs: 2049 keys 13.8 us instead of 9.6).  8 units of 128: 2048 keys 8.6 us, 13.6 us as
-// runs; 8192 keys 20.0 and 17.1 us; of 64: 8192 keys 10.0 and 13.5 us, 16384 keys
-// 15.7 and 15.1 us.
+// sequence behind a wide table takes runs: 2049 keys 13.8 us instead of 9.6).  8 units of
+// 128: 2048 keys 8.6 us, 13.6 us as runs; 8192 keys 20.0 and 17.1 us; of 64: 8192 keys 10.0
+// and 13.5 us, 16384 keys 15.7 and 15.1 us.
 // 8-bit caches: up to 12288 keys.  Of 128, one sequence of 2049 keys 13.4 us, 19.6 as runs; of
 // 12000 23.6 and 27.8; four of 12000 28.8 and 36.0; of 64, one of 12000 19.6 and 25.7.
 constexpr int64_t kClusterSteps = 12;  // of a CTA, at most
@@ -710,7 +710,8 @@ size_t paged_decode_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, in
 
 int launch_paged_decode(const lsx_tensor& q, const lsx_tensor& k_pages, const lsx_tensor& v_pages,
                         const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
-                        const int32_t* prefix_table, int64_t prefix_len, float scale, const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
+                        const int32_t* prefix_table, int64_t prefix_len, float scale,
+                        const lsx_tensor& o, const lsx_tensor& lse, void* workspace,
                         const DeviceCtx& ctx, cudaStream_t s) {
   PagedDecodeParams p;
   p.c = c;

@@ -9,7 +9,8 @@
 // of f16, and the rows' powers of two go elsewhere: a key's into its scores, a value's
 // into its weight.
 // - Q.  A row enters as f16 times a power of two that brings its largest element to
-//   [2^12, 2^13): its 8 significant bits are kept exactly down to 2^-36 of that.
+//   [2^12, 2^13): its 8 significant bits are kept exactly down to 2^-29 of that, and to
+//   half of f16's last step, 2^-37 of it, below.
 // - P.  A weight p enters as f16(p 2^(e - E + kPBits)), e the exponent of its value's row
 //   and E the largest so far (O is rescaled when it grows, as under a maximum): 11 bits,
 //   and never further off than 2^-36 of the largest that 2^E allows.  For f32 results its

@@ -41,7 +41,10 @@
 // everywhere else, so that their accuracy does not depend on how many others are
 // in the batch: P = bf16(P) + bf16(P - bf16(P)), the second half behind the first
 // in S_t's columns and multiplied with V as well.  131072 keys under 128 rows, a
-// call: heads of 128 124 us with one product, 161 with both, of 64 98 and 141.
+// call: heads of 128 124 us with one product, 161 with both, of 64 98 and 141.  Over an
+// 8-bit cache the same holds for prompts whose results are f32, by way of a bf16 copy;
+// tiles widened in place keep 11 and 22 bits (below), so that there the bits follow from
+// the number of rows, and a workspace without room for the copy keeps the more of them.
 //
 // The issuing thread and the softmax take turns in setting the pace, so both are
 // kept short (times of the 12345 tokens above, one after the other):
@@ -311,7 +314,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 // softmax goes over TMEM twice, 32 scores a turn, for the maximum and for the weights.
 // 12 sequences' 150 tokens after up to 9000 keys, 24 heads over 8 of 64: 97 us
 // (105 before; bf16, twice the bytes: 76), tensor pipe 20%, issue 47%; 131072 keys under
-// 256 rows, 8 heads of 128: 129 us (147; bf16 108), tensor pipe 44%.
+// 256 rows, 8 heads of 128: 125 us (147; bf16 108), tensor pipe 46%.
 // The rows' powers of two stay out of the softmax's loop:
 // - A tile's rows become value * 2^(e - E + kRise), E the largest exponent of the tile's
 //   rows: at most 448 * 2^7, an f16 still, exact down to e = E - 22, and below that to
@@ -319,7 +322,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 //   For keys 2^(E - kRise) is a factor of all the tile's scores, for values an exponent of
 //   all its weights.
 // - Q becomes f16 times a power of two that brings the largest element of an item's
-//   rows to [2^14, 2^15): 8 bits are kept exactly down to 2^-29 of it.
+//   rows to [2^14, 2^15): 8 bits are kept exactly down to 2^-31 of it.
 // - P is kept as f16, 11 bits.  The weights that are stored are 2^(kShift + E - E_ref) of
 //   what the row sums count, E_ref the exponent of O's unit: below f16's normal range they
 //   are off by up to 2^-33 of the row's largest, times 448 2^E_ref.  E_ref is the first
@@ -582,29 +585,29 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             ++count;
           }
         } else {
-        for (int j = 0; j <= nkv && nkv > 0; ++j) {  // step j: K of tile j, V of tile j - 1
-          const int32_t mine = next;
-          next = group_page(x, j + 1, nkv);
-          const bool exists = mine >= 0 && mine < p.c.n_pages;
-          if (j < nkv && lane < 8 && !exists && (x.e.j0 + j) * 128 + lane * 16 < x.e.len)
-            atomicCAS(p.status, 0, kStatusPage);
-          const uint32_t mask = __ballot_sync(0xffffffffu, exists) & 255u;
-          const int page = box_page(mine);
-          if (!wait_all(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
-          if (lane == 0) {
-            // (the word of 8 tiles ago: its readers are done, for the S product
-            // of the tile `stages` ago has been taken after their P)
-            if (j < nkv) *const_cast<volatile uint32_t*>(&sm.keys_ok[count % kOkRing]) = mask;
-            mbar_arrive_expect_tx(&sm.full[stage], (j > 0 && j < nkv ? 2 : 1) * C::kTileBytes);
+          for (int j = 0; j <= nkv && nkv > 0; ++j) {  // step j: K of tile j, V of tile j - 1
+            const int32_t mine = next;
+            next = group_page(x, j + 1, nkv);
+            const bool exists = mine >= 0 && mine < p.c.n_pages;
+            if (j < nkv && lane < 8 && !exists && (x.e.j0 + j) * 128 + lane * 16 < x.e.len)
+              atomicCAS(p.status, 0, kStatusPage);
+            const uint32_t mask = __ballot_sync(0xffffffffu, exists) & 255u;
+            const int page = box_page(mine);
+            if (!wait_all(&sm.empty[stage], phase ^ 1)) { ok = false; break; }
+            if (lane == 0) {
+              // (the word of 8 tiles ago: its readers are done, for the S product
+              // of the tile `stages` ago has been taken after their P)
+              if (j < nkv) *const_cast<volatile uint32_t*>(&sm.keys_ok[count % kOkRing]) = mask;
+              mbar_arrive_expect_tx(&sm.full[stage], (j > 0 && j < nkv ? 2 : 1) * C::kTileBytes);
+            }
+            __syncwarp();
+            if (j < nkv && lane < boxes * C::kSub)
+              tma_load_4d(&sm.k[stage][at], &tm_k, &sm.full[stage], sub * 64, page_row(x, j), x.hk,
+                          page);
+            if (j < nkv) ++count;
+            ++steps;
+            if (++stage == kStages) { stage = 0; phase ^= 1; }
           }
-          __syncwarp();
-          if (j < nkv && lane < boxes * C::kSub)
-            tma_load_4d(&sm.k[stage][at], &tm_k, &sm.full[stage], sub * 64, page_row(x, j), x.hk,
-                        page);
-          if (j < nkv) ++count;
-          ++steps;
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
-        }
         }
         if (!ok) break;
       }
@@ -820,7 +823,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       }
     }
   } else if (Q8 && warp >= 12) {
-      regs_dec<112>();
+    regs_dec<112>();
     if constexpr (Q8) {
       // --------------------------------------- queries and tiles to f16
       using Raw = RawTiles<D, true>;
@@ -1094,98 +1097,98 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           }
           l += ((la.x + la.y) + (lb.x + lb.y)) * ex2(-shift);
         } else {
-        float s[128];
-        {
-          uint32_t u0[32], u1[32], u2[32], u3[32];
-          tmem_ld32(tS, u0);
-          tmem_ld32(tS + 32, u1);
-          tmem_ld32(tS + 64, u2);
-          tmem_ld32(tS + 96, u3);
-          tmem_ld_wait32(u0);
-          reg_fence32(u1);
-          reg_fence32(u2);
-          reg_fence32(u3);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            s[i] = __uint_as_float(u0[i]);
-            s[32 + i] = __uint_as_float(u1[i]);
-            s[64 + i] = __uint_as_float(u2[i]);
-            s[96 + i] = __uint_as_float(u3[i]);
-          }
-        }
-        if (last < 127) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > last) s[i] = kNegInf;
-        }
-        if (okm != 255u) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (((okm >> (i / 16)) & 1u) == 0) s[i] = kNegInf;
-        }
-        auto weights = [&]() -> float {
-          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m, -m);
-          float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-          if constexpr (kSplitP) {
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 arg =
-                    __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
-                const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
-                if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
-                hi[i] = pack_bf16(e.x, e.y);
-                lo[i] = pack_bf16(e.x - __uint_as_float(hi[i] << 16),
-                                  e.y - __uint_as_float(hi[i] & 0xffff0000u));
-              }
-              tmem_st16(tS + cc * 16, hi);
-              tmem_st16(tS + 64 + cc * 16, lo);
-            }
-          } else {
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t pk[32];
+          float s[128];
+          {
+            uint32_t u0[32], u1[32], u2[32], u3[32];
+            tmem_ld32(tS, u0);
+            tmem_ld32(tS + 32, u1);
+            tmem_ld32(tS + 64, u2);
+            tmem_ld32(tS + 96, u3);
+            tmem_ld_wait32(u0);
+            reg_fence32(u1);
+            reg_fence32(u2);
+            reg_fence32(u3);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float2 arg =
-                  __ffma2_rn(make_float2(s[cc * 64 + 2 * i], s[cc * 64 + 2 * i + 1]), sc2, nm2);
-              const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
-              if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
-              pk[i] = pack_bf16(e.x, e.y);
+              s[i] = __uint_as_float(u0[i]);
+              s[32 + i] = __uint_as_float(u1[i]);
+              s[64 + i] = __uint_as_float(u2[i]);
+              s[96 + i] = __uint_as_float(u3[i]);
             }
-            tmem_st32(tS + cc * 32, pk);
           }
-          }
-          return (la.x + la.y) + (lb.x + lb.y);
-        };
-        float part = weights();  // the tile's row sum under m
-        const bool few = first && last < 127;  // the row ends in this tile
-        if (__any_sync(0xffffffffu, live && (few || !(part < kMostSum && l + part > kLeastSum)))) {
-          float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+          if (last < 127) {
 #pragma unroll
-          for (int i = 4; i < 124; i += 8) {
-            mx0 = fmax3(mx0, s[i], s[i + 1]);
-            mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
-            mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
-            mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
+            for (int i = 0; i < 128; ++i)
+              if (i > last) s[i] = kNegInf;
           }
-          mx0 = fmax3(mx0, s[124], s[125]);
-          mx1 = fmax3(mx1, s[126], s[127]);
-          const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
-          // m to the size of what the row has, or gets: alpha is at most 1 / l
-          float m_new = fmaxf(l > 0.f ? m + lg2(l) : kNegInf, mx * sl2);
-          if (!(m_new > kNegInf)) m_new = m;
-          // the weights stored first have landed before others follow them
-          tmem_st_wait();
-          if (!first) {
-            if (!rescale(m_new, 1.f)) { ok = false; break; }
+          if (okm != 255u) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (((okm >> (i / 16)) & 1u) == 0) s[i] = kNegInf;
           }
-          m = m_new;
-          part = weights();
-        }
-        l += part;
+          auto weights = [&]() -> float {
+            const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m, -m);
+            float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+            if constexpr (kSplitP) {
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 arg =
+                      __ffma2_rn(make_float2(s[cc * 32 + 2 * i], s[cc * 32 + 2 * i + 1]), sc2, nm2);
+                  const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
+                  if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
+                  hi[i] = pack_bf16(e.x, e.y);
+                  lo[i] = pack_bf16(e.x - __uint_as_float(hi[i] << 16),
+                                    e.y - __uint_as_float(hi[i] & 0xffff0000u));
+                }
+                tmem_st16(tS + cc * 16, hi);
+                tmem_st16(tS + 64 + cc * 16, lo);
+              }
+            } else {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 arg =
+                    __ffma2_rn(make_float2(s[cc * 64 + 2 * i], s[cc * 64 + 2 * i + 1]), sc2, nm2);
+                const float2 e = make_float2(ex2(arg.x), ex2(arg.y));
+                if (i & 1) lb = __fadd2_rn(lb, e); else la = __fadd2_rn(la, e);
+                pk[i] = pack_bf16(e.x, e.y);
+              }
+              tmem_st32(tS + cc * 32, pk);
+            }
+            }
+            return (la.x + la.y) + (lb.x + lb.y);
+          };
+          float part = weights();  // the tile's row sum under m
+          const bool few = first && last < 127;  // the row ends in this tile
+          if (__any_sync(0xffffffffu, live && (few || !(part < kMostSum && l + part > kLeastSum)))) {
+            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+            for (int i = 4; i < 124; i += 8) {
+              mx0 = fmax3(mx0, s[i], s[i + 1]);
+              mx1 = fmax3(mx1, s[i + 2], s[i + 3]);
+              mx2 = fmax3(mx2, s[i + 4], s[i + 5]);
+              mx3 = fmax3(mx3, s[i + 6], s[i + 7]);
+            }
+            mx0 = fmax3(mx0, s[124], s[125]);
+            mx1 = fmax3(mx1, s[126], s[127]);
+            const float mx = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+            // m to the size of what the row has, or gets: alpha is at most 1 / l
+            float m_new = fmaxf(l > 0.f ? m + lg2(l) : kNegInf, mx * sl2);
+            if (!(m_new > kNegInf)) m_new = m;
+            // the weights stored first have landed before others follow them
+            tmem_st_wait();
+            if (!first) {
+              if (!rescale(m_new, 1.f)) { ok = false; break; }
+            }
+            m = m_new;
+            part = weights();
+          }
+          l += part;
         }
         first = false;
         tmem_st_wait();
@@ -1756,9 +1759,9 @@ size_t paged_fwd_workspace(const lsx_tensor& q, const lsx_tensor& k_pages, int64
 
 int launch_paged_fwd(const lsx_tensor& q, const lsx_tensor& pages_k, const lsx_tensor& pages_v,
                      const PagedCache& c, const PagedCache8* c8, const int32_t* kv_lens,
-                     const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o, const lsx_tensor& lse,
-                     void* workspace, size_t workspace_bytes, const DeviceCtx& ctx,
-                     cudaStream_t s) {
+                     const int32_t* cu_q, int64_t batch, float scale, const lsx_tensor& o,
+                     const lsx_tensor& lse, void* workspace, size_t workspace_bytes,
+                     const DeviceCtx& ctx, cudaStream_t s) {
   const bool split_p = c8 != nullptr && o.dtype == LSX_F32;
   FwdLayout x = fwd_layout(q, pages_k, batch, c.max_pages, c8 != nullptr, ctx.sm_count);
   if (workspace_bytes < x.total)  // no room for the copy: the caller goes without

@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(256) page_read_q8_kernel(const ReadQ8Params p)
 // A bf16 copy of the pages that a call's prompts see, for many query rows a key: the
 // prompt kernel then reads tiles that its products take as they are.  Every block sums the
 // sequences' pages for itself and takes pieces of pages in turn (a whole page: a tenth
-// more, 298 us instead of 288 for the call below).  Bound: HBM (what it writes is read
-// again at once, from L2 as far as it holds it).  256 tokens after 65536 keys, 32 query
-// heads over 8 of 128: 65 us for 0.14 GB read and 0.27 written (0.21 of them to DRAM),
+// more, 298 us instead of 288 for 256 tokens after 65536 keys, 32 query heads over 8 of
+// 128).  Bound: HBM (what it writes is read again at once, from L2 as far as it holds it).
+// These 65,792 keys: 65 us for 0.14 GB read and 0.27 written (0.21 of them to DRAM),
 // 5.3 TB/s of DRAM.
 constexpr int kWidenCtas = 4;      // on an SM at once
 constexpr int kWidenPieces = 512;  // 16-byte pieces of keys (and of values) in a block's turn
